@@ -483,6 +483,162 @@ int fathom_union_attention(const void* k_cache, const void* v_cache, int kv_dtyp
                            float* out, void* workspace, size_t ws_bytes, fathom_stream_t stream);
 
 /*
+ * The paged KV cache: the session's keys and values in pages, in 16 bits or
+ * quantised to 8 as they are written, for the attention that runs beside the
+ * scan (dense prompt chunks and tokens, and the union of the scan's
+ * winners).  (The paper keeps a full-precision cache; the 8-bit rows and the
+ * pages are this library's own.)
+ *
+ * A cached row is one token of one group, D channels.  Formats:
+ *   FATHOM_KV_BF16  the row in bf16 (fp32 input rounded to nearest even).
+ *   FATHOM_KV_INT8  per 32 channels one power of two 2^e and int8 codes
+ *                   c = rint(x 2^-e), |c| <= 127 (ties to even): e is the
+ *                   least with rint(m 2^-e) <= 127, m the block's largest
+ *                   magnitude.  Value c 2^e.
+ *   FATHOM_KV_E4M3  the same with codes the 8-bit float (4 exponent, 3
+ *                   mantissa bits, largest 448) nearest to x 2^-e, ties to
+ *                   even: e is the least with m 2^-e <= 464, the last value
+ *                   that rounds to 448.
+ * e is kept as the byte e + 127, -100 <= e <= 121 (INT8) or 7 (E4M3: larger
+ * magnitudes than 448 * 2^7 become +-57344); m = 0 gives e = -100.  A block
+ * with an infinity or a NaN is kept as byte 255 and reads back as NaN.  Every
+ * value is exact in bf16, so the operators below see a bf16 cache: they
+ * round nothing when they decode.
+ *
+ *   k, v            DEVICE, element (page, group, token, channel) of the pages at
+ *                   page*page_stride + group*head_stride + token*token_stride
+ *                   + channel (element units; INT8 and E4M3 elements are one
+ *                   byte).  16-byte aligned, and so is every stride in bytes.
+ *   k_scale, v_scale  DEVICE, uint8: the exponent byte of channels 32i .. 32i+31
+ *                   at page*scale_page_stride + group*scale_head_stride +
+ *                   token*scale_token_stride + i.  Not used with BF16.
+ *                   4-byte aligned strides and pointers where D % 128 == 0.
+ *   pages, H, D, page_tokens  D as elsewhere; page_tokens 16, 32, 64, 128 or 256;
+ *                   H <= 65535; pages < 2^31.
+ * The strides make a page hold [H][page_tokens][D], [page_tokens][H][D], or
+ * one layer of a cache of many.
+ */
+#define FATHOM_KV_BF16 0
+#define FATHOM_KV_INT8 1
+#define FATHOM_KV_E4M3 2
+
+typedef struct fathom_kv_cache {
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int64_t pages;
+    int64_t page_stride, head_stride, token_stride;
+    int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+    int32_t H, D, page_tokens, format;
+} fathom_kv_cache;
+
+/*
+ * The rows of a call: those of B sequences, one after another.  Rows
+ * cu[b] .. cu[b+1]-1 are the LAST tokens of sequence b up to its length:
+ * row r is the token at position length[b] - cu[b+1] + r, kept in page
+ * table[b*table_stride + position / page_tokens].
+ *   table           DEVICE, int32 [B][table_pages], rows table_stride apart.
+ *   cu              DEVICE, int32 [B+1], from 0, not decreasing.
+ *   length          DEVICE, int32 [B]: the sequence's tokens, the call's
+ *                   rows among them.
+ *   rows            rows of the call's arrays; those from cu[B] on are neither
+ *                   read nor written.
+ * A position below 0 or beyond table_pages pages, and a page id outside
+ * [0, pages), name no token: nothing is written there, it reads as zeros,
+ * and attention leaves it out.
+ * B <= 65535; rows < 2^31.
+ */
+typedef struct fathom_kv_rows {
+    const int32_t* table;
+    const int32_t* cu;
+    const int32_t* length;
+    int64_t table_stride, rows;
+    int32_t table_pages, B;
+} fathom_kv_rows;
+
+/*
+ * fathom_kv_write -- put rows into the cache, in its format.
+ *
+ *   k, v            DEVICE, FATHOM_KEYS_F32 or FATHOM_KEYS_BF16 elements; row r of
+ *                   group h, channel j at [r*stride_tok + h*stride_h + j].
+ * The pages written must not be shared by two sequences of the call: of
+ * two rows for one place each block keeps either's codes and scale, not
+ * always of the same one.
+ */
+int fathom_kv_write(const fathom_kv_cache* cache, const fathom_kv_rows* rows, const void* k, const void* v,
+                    int dtype, int64_t stride_tok, int64_t stride_h, fathom_stream_t stream);
+
+/*
+ * fathom_kv_read -- rows back out of the cache: to
+ * out[h*stride_h + r*stride_tok + j], fp32 or bf16 (exact in both), the
+ * layout that fathom_pack, fathom_calibrate and fathom_union_attention take.
+ *
+ *   out_k, out_v    DEVICE out; either may be NULL.
+ */
+int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, void* out_k, void* out_v, int dtype,
+                   int64_t stride_h, int64_t stride_tok, fathom_stream_t stream);
+
+/*
+ * fathom_paged_attention -- attention of each sequence's new rows over its
+ * cached tokens, the rows' own among them (write them first): a chunk of a
+ * prompt, or single tokens.  For row r of sequence b at position p, query
+ * head g of group h, over the tokens i of the sequence (i <= p when causal):
+ *   s_i = scale * q_{r,h,g} . K_{i,h},   out = sum_i softmax(s)_i V_{i,h}.
+ * A row that sees no token gives zeros.
+ *
+ *   q               DEVICE, FATHOM_KEYS_F32 or FATHOM_KEYS_BF16: head g of group h of
+ *                   row r at [r*q_stride_tok + (h*G + g)*q_stride_h + j].
+ *   max_new         rows of a sequence that are computed at most (the others'
+ *                   outputs are left as they were).
+ *   max_len         cached tokens of a sequence that are read at most.
+ *                   Both size the launch: give the batch's largest, or a bound
+ *                   that holds for every replay of a captured graph.
+ *   scale           usually 1/sqrt(D); finite.
+ *   out             DEVICE out, [rows][H][G][D], of q's type.
+ *   workspace, ws_bytes  DEVICE scratch of at least
+ *                   fathom_paged_attention_workspace_bytes() bytes for the
+ *                   same H, G, D, rows, B, max_new, max_len, q_dtype, 256-byte
+ *                   aligned (may be NULL when that is 0).  Used until the
+ *                   call's work is done: calls that may overlap on the GPU
+ *                   need one each.
+ * Arithmetic: products of bf16 values summed in fp32, the softmax in fp32.
+ * fp32 queries are taken as the sum of three bf16 parts (all 24 bits); the
+ * weights exp(s - max) enter the value product in bf16 for bf16 queries of
+ * prompt chunks, in two bf16 parts (16 bits) for bf16 queries otherwise, and in three for
+ * fp32 queries.  Cached values of tokens below length should be finite where
+ * rows that do not see them are to stay finite; what lies beyond length in
+ * a page is never used.  1 <= G <= 8.
+ */
+size_t fathom_paged_attention_workspace_bytes(int H, int G, int D, int64_t rows, int B, int64_t max_new,
+                                              int64_t max_len, int q_dtype);
+
+int fathom_paged_attention(const fathom_kv_cache* cache, const fathom_kv_rows* rows, const void* q, int q_dtype,
+                           int64_t q_stride_tok, int64_t q_stride_h, int G, int64_t max_new, int64_t max_len,
+                           int causal, float scale, void* out, void* workspace, size_t ws_bytes,
+                           fathom_stream_t stream);
+
+/*
+ * fathom_paged_union_attention -- fathom_union_attention with the winners'
+ * rows taken from one sequence of the paged cache.
+ *
+ *   table           DEVICE, int32 [table_pages]: the sequence's pages.
+ *   n               tokens that an index may name: 0 <= i < n (others, and those of
+ *                   pages that name no token, are skipped).
+ *   q, union_idx, union_count, M, scale, out
+ *                   as for fathom_union_attention (fp32, H = cache->H groups).
+ *   workspace, ws_bytes  DEVICE scratch of at least
+ *                   fathom_paged_union_attention_workspace_bytes(H, G, D, M)
+ *                   bytes, 256-byte aligned (may be NULL when that is 0).
+ */
+size_t fathom_paged_union_attention_workspace_bytes(int64_t H, int G, int D, int64_t M);
+
+int fathom_paged_union_attention(const fathom_kv_cache* cache, const int32_t* table, int32_t table_pages, int64_t n,
+                                 const float* q, int G, const int32_t* union_idx, const int32_t* union_count,
+                                 int64_t M, float scale, float* out, void* workspace, size_t ws_bytes,
+                                 fathom_stream_t stream);
+
+/*
  * fathom_scan_topk_noalloc -- fathom_scan in CANDIDATE mode followed by
  * fathom_topk, for callers that cannot allocate device memory.  (The paper
  * has no counterpart: this is a deployment convenience of this library.)

@@ -5,8 +5,7 @@
 // (noalloc.cu).  Every entry point that enqueues work opens an NVTX range
 // named after it, so that a trace shows the library's calls on the host
 // timeline (a no-op unless a profiler is attached).
-#include <nvtx3/nvToolsExt.h>
-
+#include "args.cuh"
 #include "common.cuh"
 
 namespace fathom {
@@ -50,14 +49,6 @@ int launch_union_attention(const void* k, const void* v, int kv_dtype, int64_t H
 
 static thread_local int g_last_cuda_error = 0;
 
-// NVTX range over one library call.
-struct NvtxRange {
-    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange&) = delete;
-    NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
 int cuda_status(cudaError_t e)
 {
     if (e == cudaSuccess) return FATHOM_OK;
@@ -66,32 +57,6 @@ int cuda_status(cudaError_t e)
 }
 
 namespace {
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// A pointer the current device can dereference: device or managed memory,
-// or page-locked host memory mapped into the device's address space.
-int check_device_ptr(const void* p)
-{
-    if (!p) return FATHOM_ERR_INVALID_ARG;
-    cudaPointerAttributes attr;
-    const cudaError_t e = cudaPointerGetAttributes(&attr, p);
-    if (e != cudaSuccess) {
-        (void)cudaGetLastError();
-        return FATHOM_ERR_INVALID_ARG;
-    }
-    switch (attr.type) {
-        case cudaMemoryTypeDevice:
-        case cudaMemoryTypeManaged:
-            return FATHOM_OK;
-        case cudaMemoryTypeHost:
-            return attr.devicePointer == p ? FATHOM_OK : FATHOM_ERR_INVALID_ARG;
-        default:
-            return FATHOM_ERR_INVALID_ARG;
-    }
-}
-
-bool dims_ok(int D, int G) { return D >= 32 && D <= kMaxD && D % 32 == 0 && G >= 1 && G <= kMaxG; }
 
 #define FATHOM_TRY_IN(expr)              \
     do {                                 \

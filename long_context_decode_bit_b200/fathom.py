@@ -32,6 +32,10 @@ SCAN_DENSE = 0
 SCAN_CANDIDATE = 1
 SCAN_PREPARE = 2
 SCAN_FILTER = 3
+KV_BF16 = 0
+KV_INT8 = 1
+KV_E4M3 = 2
+KV_BLOCK = 32     # channels that share a power of two
 
 # Every symbol include/fathom.h declares.
 EXPORTS = (
@@ -42,6 +46,8 @@ EXPORTS = (
     "fathom_union_attention_workspace_bytes", "fathom_union_attention",
     "fathom_nibbles_from_planes", "fathom_scan_nibbles", "fathom_layer_budgets_workspace_bytes",
     "fathom_layer_budgets", "fathom_pack_rotated", "fathom_nibbles_tm_from_planes", "fathom_scan_nibbles_tm",
+    "fathom_kv_write", "fathom_kv_read", "fathom_paged_attention_workspace_bytes", "fathom_paged_attention",
+    "fathom_paged_union_attention_workspace_bytes", "fathom_paged_union_attention",
 )
 
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -69,7 +75,7 @@ def load(path: str | None = None):
         raise FileNotFoundError(
             f"{path} is missing: build it with `python -m long_context_decode_bit_b200.build`")
     lib = ctypes.CDLL(path)
-    P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    P, I, I64, SZ, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     sig = {
         "fathom_version": (I, []),
         "fathom_status_string": (ctypes.c_char_p, [I]),
@@ -96,6 +102,12 @@ def load(path: str | None = None):
         "fathom_layer_budgets": (I, [P, P, I64, I, I, I, I64, P, P, SZ, P]),
         "fathom_scan_nibbles": (I, [P, P, I64, I, I64, I64, P, P, P, I, I, P, P, SZ, I, P]),
         "fathom_union_attention": (I, [P, P, I, I64, I64, I, I64, I64, P, I, P, P, I64, ctypes.c_float, P, P, SZ, P]),
+        "fathom_kv_write": (I, [P, P, P, P, I, I64, I64, P]),
+        "fathom_kv_read": (I, [P, P, P, P, I, I64, I64, P]),
+        "fathom_paged_attention_workspace_bytes": (SZ, [I, I, I, I64, I, I64, I64, I]),
+        "fathom_paged_attention": (I, [P, P, P, I, I64, I64, I, I64, I64, I, F, P, P, SZ, P]),
+        "fathom_paged_union_attention_workspace_bytes": (SZ, [I64, I, I, I64]),
+        "fathom_paged_union_attention": (I, [P, P, ctypes.c_int32, I64, P, I, P, P, I64, F, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -393,6 +405,209 @@ def union_attention(k_cache: torch.Tensor, v_cache: torch.Tensor, q: torch.Tenso
     _check(lib().fathom_union_attention(_p(k_cache), _p(v_cache), dt, H, n, D, k_cache.stride(0), k_cache.stride(1),
                                         _p(q), G, _p(union_idx), _p(union_count), M, sc, _p(out), _p(workspace),
                                         workspace.numel(), _stream(stream)), "fathom_union_attention")
+    return out
+
+
+class _KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("scale_token_stride", ctypes.c_int64), ("H", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class _KvRowsStruct(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("cu", ctypes.c_void_p), ("length", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("rows", ctypes.c_int64), ("table_pages", ctypes.c_int32),
+                ("B", ctypes.c_int32)]
+
+
+_KV_FORMATS = {torch.bfloat16: KV_BF16, torch.int8: KV_INT8, torch.float8_e4m3fn: KV_E4M3}
+_KEY_TYPES = {torch.float32: KEYS_F32, torch.bfloat16: KEYS_BF16}
+
+
+class KVCache:
+    """A paged KV cache over the caller's tensors (fathom_kv_cache in
+    include/fathom.h): k, v [pages][H][page_tokens][D] in bf16, int8 or
+    float8_e4m3fn (any strides, channels contiguous; ``transpose(1, 2)`` of a
+    [pages][page_tokens][H][D] tensor, or one layer of a larger one), and for
+    the 8-bit formats k_scale, v_scale uint8 [pages][H][page_tokens][D/32]."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale=None, v_scale=None):
+        if k.dtype not in _KV_FORMATS:
+            raise TypeError("the cache is bfloat16, int8 or float8_e4m3fn")
+        if k.dim() != 4 or v.dtype != k.dtype or v.shape != k.shape or v.stride() != k.stride() or v.device != k.device:
+            raise ValueError("k and v must be [pages][H][page_tokens][D] and share dtype, strides and device")
+        if k.stride(3) != 1:
+            raise ValueError("the cache must be contiguous along D")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.format = _KV_FORMATS[k.dtype]
+        pages, self.H, self.page_tokens, self.D = k.shape
+        strides = (0, 0, 0)
+        if self.format != KV_BF16:
+            shape = (pages, self.H, self.page_tokens, self.D // KV_BLOCK)
+            for s in (k_scale, v_scale):
+                if s is None or s.dtype != torch.uint8 or tuple(s.shape) != shape or s.device != k.device:
+                    raise ValueError("an 8-bit cache needs uint8 scales [pages][H][page_tokens][D/32] beside it")
+            if k_scale.stride() != v_scale.stride() or k_scale.stride(3) != 1:
+                raise ValueError("the scales must share strides and be contiguous along D/32")
+            strides = k_scale.stride()[:3]
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        scale_ptr = (None, None) if k_scale is None else (k_scale.data_ptr(), v_scale.data_ptr())
+        self._struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), *scale_ptr, pages, k.stride(0), k.stride(1),
+                                      k.stride(2), strides[0], strides[1], strides[2], self.H, self.D,
+                                      self.page_tokens, self.format)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, pages: int, H: int, D: int, page_tokens: int = 64, dtype=torch.int8, device="cuda"):
+        """A cache of zeros."""
+        shape = (pages, H, page_tokens, D)
+        if dtype == torch.float8_e4m3fn:
+            k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
+        else:
+            k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+        if dtype == torch.bfloat16:
+            return cls(k, v)
+        return cls(k, v, *(torch.zeros(shape[:3] + (D // KV_BLOCK,), dtype=torch.uint8, device=device)
+                           for _ in range(2)))
+
+
+def _kv_here(cache: KVCache, *tensors):
+    """Tensors of a cache call live on the cache's device, and that is the current one."""
+    dev = cache.k.device
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError("the tensors of a call must be on the cache's device")
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError("the cache must be on the current CUDA device")
+
+
+def _kv_rows(cache: KVCache, table, cu, length, rows: int):
+    B = length.shape[0]
+    if table.dtype != torch.int32 or cu.dtype != torch.int32 or length.dtype != torch.int32:
+        raise TypeError("table, cu and length are int32")
+    if table.dim() != 2 or table.shape[0] != B or cu.shape != (B + 1,) or length.dim() != 1:
+        raise ValueError("table is [B][pages], cu [B+1] and length [B]")
+    if not (cu.is_contiguous() and length.is_contiguous() and (table.shape[1] < 2 or table.stride(1) == 1)):
+        raise ValueError("table rows, cu and length must be contiguous")
+    _kv_here(cache, table, cu, length)
+    return ctypes.byref(_KvRowsStruct(table.data_ptr(), cu.data_ptr(), length.data_ptr(), table.stride(0), rows,
+                                      table.shape[1], B))
+
+
+def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, cu: torch.Tensor,
+             length: torch.Tensor, stream=None) -> KVCache:
+    """Put rows k, v [rows][H][D] (fp32 or bf16) into the cache: the last
+    cu[b+1] - cu[b] tokens of each sequence b, up to length[b] (page table
+    int32 [B][pages], cu int32 [B+1], length int32 [B])."""
+    if k.dtype not in _KEY_TYPES or v.dtype != k.dtype:
+        raise TypeError("k and v are float32 or bfloat16")
+    if k.dim() != 3 or k.shape[1:] != (cache.H, cache.D) or v.shape != k.shape or v.stride() != k.stride():
+        raise ValueError("k and v must be [rows][H][D] and share strides")
+    if k.stride(2) != 1:
+        raise ValueError("k and v must be contiguous along D")
+    rows = _kv_rows(cache, table, cu, length, k.shape[0])
+    _kv_here(cache, k, v)
+    _check(lib().fathom_kv_write(cache._ref, rows, k.data_ptr(), v.data_ptr(), _KEY_TYPES[k.dtype], k.stride(0),
+                                 k.stride(1), _stream(stream)), "fathom_kv_write")
+    return cache
+
+
+def kv_read(cache: KVCache, table: torch.Tensor, cu: torch.Tensor, length: torch.Tensor, rows: int,
+            dtype=torch.bfloat16, out=None, stream=None):
+    """Read the same rows back: (K, V), each [H][rows][D] in ``dtype`` (fp32
+    or bf16), the layout ``pack`` takes.  ``out`` may give both tensors (any
+    strides, channels contiguous), or None in the place of one not wanted."""
+    if out is None:
+        out = tuple(torch.empty((cache.H, rows, cache.D), dtype=dtype, device=cache.k.device) for _ in range(2))
+    given = [t for t in out if t is not None]
+    for t in given:
+        if t.dtype not in _KEY_TYPES or t.dtype != given[0].dtype:
+            raise TypeError("K and V are read back in float32 or bfloat16")
+        if t.shape != (cache.H, rows, cache.D) or t.stride() != given[0].stride() or t.stride(2) != 1:
+            raise ValueError("out must be [H][rows][D] tensors of the same strides, contiguous along D")
+    if not given:
+        raise ValueError("nothing to read")
+    w = _kv_rows(cache, table, cu, length, rows)
+    _kv_here(cache, *given)
+    _check(lib().fathom_kv_read(cache._ref, w, *(None if t is None else t.data_ptr() for t in out),
+                                _KEY_TYPES[given[0].dtype], given[0].stride(0), given[0].stride(1), _stream(stream)),
+           "fathom_kv_read")
+    return tuple(out)
+
+
+def paged_attention_workspace_bytes(H: int, G: int, D: int, rows: int, B: int, max_new: int, max_len: int,
+                                    dtype=torch.bfloat16) -> int:
+    return int(lib().fathom_paged_attention_workspace_bytes(H, G, D, rows, B, max_new, max_len, _KEY_TYPES[dtype]))
+
+
+def _workspace(workspace, need: int, device):
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is None:
+        return None, None, 0
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def paged_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, cu: torch.Tensor, length: torch.Tensor,
+                    max_new: int, max_len: int, causal: bool = True, scale: float | None = None, out=None,
+                    workspace=None, stream=None) -> torch.Tensor:
+    """Attention of each sequence's new rows q [rows][H*G][D] (fp32 or bf16;
+    head h*G + g belongs to KV head h) over its cached tokens, the rows' own
+    among them: a prompt chunk or single tokens.  ``max_new`` and
+    ``max_len`` bound the batch's rows and lengths.  Returns [rows][H*G][D]."""
+    if q.dtype not in _KEY_TYPES:
+        raise TypeError("q is float32 or bfloat16")
+    if q.dim() != 3 or q.shape[2] != cache.D or q.shape[1] % cache.H or q.stride(2) != 1:
+        raise ValueError("q must be [rows][H*G][D], contiguous along D")
+    rows, G = q.shape[0], q.shape[1] // cache.H
+    if out is None:
+        out = torch.empty((rows, q.shape[1], cache.D), dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [rows][H*G][D] tensor of q's type")
+    w = _kv_rows(cache, table, cu, length, rows)
+    _kv_here(cache, q, out)
+    B, dt = length.shape[0], _KEY_TYPES[q.dtype]
+    L = lib()
+    need = L.fathom_paged_attention_workspace_bytes(cache.H, G, cache.D, rows, B, max_new, max_len, dt)
+    workspace, ws, ws_bytes = _workspace(workspace, need, q.device)
+    sc = cache.D ** -0.5 if scale is None else float(scale)
+    _check(L.fathom_paged_attention(cache._ref, w, q.data_ptr(), dt, q.stride(0), q.stride(1), G, max_new, max_len,
+                                    int(causal), sc, out.data_ptr(), ws, ws_bytes, _stream(stream)),
+           "fathom_paged_attention")
+    return out
+
+
+def paged_union_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, n: int, union_idx: torch.Tensor,
+                          union_count: torch.Tensor, scale: float | None = None, out=None, workspace=None,
+                          stream=None) -> torch.Tensor:
+    """``union_attention`` with the winners' rows taken from one sequence of
+    the paged cache: q fp32 [H][G][D], table int32 [pages] (or [1][pages]),
+    n tokens.  Returns fp32 [H][G][D]."""
+    table = table.reshape(-1)
+    if q.dtype != torch.float32 or q.dim() != 3 or q.shape[0] != cache.H or q.shape[2] != cache.D or not q.is_contiguous():
+        raise ValueError("q must be a contiguous fp32 [H][G][D] tensor")
+    if table.dtype != torch.int32 or union_idx.dtype != torch.int32 or union_count.dtype != torch.int32:
+        raise TypeError("table, union_idx and union_count are int32")
+    if union_idx.dim() != 2 or union_idx.shape[0] != cache.H or union_count.shape != (cache.H,) or \
+            not (union_idx.is_contiguous() and union_count.is_contiguous() and table.is_contiguous()):
+        raise ValueError("union_idx must be [H][M] and union_count [H], as topk writes them")
+    G, M = q.shape[1], union_idx.shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous fp32 [H][G][D] tensor")
+    _kv_here(cache, q, table, union_idx, union_count, out)
+    L = lib()
+    workspace, ws, ws_bytes = _workspace(
+        workspace, L.fathom_paged_union_attention_workspace_bytes(cache.H, G, cache.D, M), q.device)
+    sc = cache.D ** -0.5 if scale is None else float(scale)
+    _check(L.fathom_paged_union_attention(cache._ref, table.data_ptr(), table.numel(), n, q.data_ptr(), G,
+                                          union_idx.data_ptr(), union_count.data_ptr(), M, sc, out.data_ptr(), ws,
+                                          ws_bytes, _stream(stream)), "fathom_paged_union_attention")
     return out
 
 
