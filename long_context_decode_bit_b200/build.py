@@ -53,7 +53,7 @@ def build(force: bool = False, ptxas_verbose: bool = False, test_hooks: bool = F
     lib = TEST_LIB if test_hooks else LIB
     if not force and not _stale(lib):
         return lib
-    cmd = [nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), "-O3", "-std=c++17", "--threads", "0", *ARCH, "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
            "-I", INCLUDE, "-I", CSRC, *(TEST_DEFINES if test_hooks else []), "-o", lib, *sources()]
     if ptxas_verbose:
         cmd.insert(1, "-Xptxas=-v")

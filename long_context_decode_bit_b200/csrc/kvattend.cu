@@ -1,162 +1,154 @@
-// fathom_paged_attention and fathom_paged_union_attention: softmax attention
-// of a group's query heads over rows of the paged cache.
-//
-// One CTA per (row of queries, group): warp w scores the keys w, w + 8, ...
-// with its lanes across the channels and keeps a running maximum, weight sum
-// and value sum per head; the eight warps' results are joined at the end.
-#include "kv.cuh"
+// fathom_paged_attention and fathom_paged_union_attention: how a call is cut
+// up, and the joining of its stretches.
+#include <algorithm>
+
+#include "kvrows.cuh"
 
 namespace fathom {
 
 namespace {
 
-constexpr int kSimpleWarps = 8;
+constexpr int kSms = 148;        // the machine this library is written for; only the cut depends on it
+constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps = kJoinThreads / 32;
 
-template <int FMT>
-__device__ __forceinline__ float kv_value(const unsigned char* data, int j, uint32_t byte)
+int64_t round_up(int64_t x, int64_t to) { return ceil_div(x, to) * to; }
+
+// Rows of 8*nt query rows by stretches of tokens.  A CTA's four warps want
+// 64 tokens at least each; four CTAs fit an SM.
+KvSplit rows_split(int H, int G, int D, int B, int64_t max_new, int64_t max_len)
 {
-    if (FMT == FATHOM_KV_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(data)[j]);
-    if (FMT == FATHOM_KV_INT8) return static_cast<float>(reinterpret_cast<const int8_t*>(data)[j]) * kv_pow2(byte);
-    const __half_raw r = __nv_cvt_fp8_to_halfraw(data[j], __NV_E4M3);
-    return __half2float(__half(r)) * kv_pow2(byte);
+    KvSplit s{};
+    const int64_t qrows = max_new * G;
+    s.nt = qrows <= 8 ? 1 : (D <= 128 ? 4 : 2);
+    s.row_tiles = static_cast<int32_t>(ceil_div(qrows, 8 * s.nt));
+    const int64_t items = static_cast<int64_t>(B) * H * s.row_tiles;
+    // One session: its stretches are equal, one wave of CTAs.  Several of uneven
+    // lengths: shorter stretches, so that the longest session does not end alone.
+    const int64_t want = B == 1 ? 4 * kSms : 32 * kSms;
+    const int64_t splits = std::max<int64_t>(1, want / items);
+    int64_t chunk = round_up(ceil_div(std::max<int64_t>(max_len, 1), splits), 64);
+    if (chunk < 256) chunk = 256;
+    s.chunk = static_cast<int32_t>(chunk);
+    s.splits = static_cast<int32_t>(ceil_div(std::max<int64_t>(max_len, 1), chunk));
+    return s;
 }
 
-template <int FMT, int QT, bool UNION>
-__global__ void __launch_bounds__(32 * kSimpleWarps)
-kv_attend_kernel(const KvAttend a)
+KvSplit union_split(int64_t H, int64_t M)
 {
-    extern __shared__ float sm[];   // [warps][G][D] value sums, [warps][G] maxima, [warps][G] weight sums
-    const int G = a.G, D = a.c.D;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y;
-    const int row = blockIdx.x;
-    const int32_t* table = a.w.table;
-    int64_t keys;
-    if (UNION) {
-        keys = min(static_cast<int64_t>(max(a.count[h], 0)), a.M);
+    KvSplit s{1, 1, 1, 0};
+    const int64_t splits = std::max<int64_t>(1, 4 * kSms / H);
+    s.chunk = static_cast<int32_t>(std::max<int64_t>(round_up(ceil_div(M, splits), 64), 64));
+    s.splits = static_cast<int32_t>(ceil_div(M, s.chunk));
+    return s;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+size_t parts_bytes(int64_t heads, int64_t splits, int D)
+{
+    return splits > 1 ? up256(sizeof(float) * splits * heads * D) + 2 * up256(sizeof(float) * splits * heads) : 0;
+}
+
+// One CTA per query head of a row: the stretches' value sums, each times
+// 2^(its maximum - the largest), over the weight sums treated alike.
+template <int QT>
+__global__ void __launch_bounds__(kJoinThreads)
+kv_join_kernel(const KvRowsArgs g)
+{
+    __shared__ float part[kJoinWarps][kMaxD];
+    __shared__ float part_l[kJoinWarps];
+    pdl_wait();
+    const KvAttend& a = g.a;
+    const int D = a.c.D, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x;
+    const int64_t head = row * gridDim.y + blockIdx.y;
+    int n;   // stretches that were computed
+    if (a.uni) {
+        const int h = blockIdx.y / a.G;
+        n = static_cast<int>(ceil_div(min(static_cast<int64_t>(max(a.count[h], 0)), a.M), g.s.chunk));
     } else {
-        const int b = kv_sequence(a.w, row);
+        const int b = kv_sequence(a.w, static_cast<int>(row));
         if (b < 0) return;
-        const int64_t first = a.w.cu[b], end = a.w.cu[b + 1], len = a.w.length[b];
-        if (row - first >= a.max_new) return;
-        const int64_t pos = len - end + row;
-        keys = max(int64_t{0}, min(min(a.causal ? pos + 1 : len, len), a.max_len));
-        table += b * a.w.table_stride;
+        const KvSpan sp = kv_span(a, b);
+        const int qr = static_cast<int>(row - sp.first) * a.G + blockIdx.y % a.G;
+        if (row - sp.first >= sp.rows) return;
+        const int r0 = qr / (8 * g.s.nt) * 8 * g.s.nt;
+        n = static_cast<int>(ceil_div(kv_tile_keys(a, sp, r0, 8 * g.s.nt), g.s.chunk));
     }
-    float qv[kMaxG][kMaxD / 32], o[kMaxG][kMaxD / 32], m[kMaxG], l[kMaxG];
+    float top = -INFINITY;
+    for (int s = lane; s < n; s += 32) top = fmaxf(top, g.pm[s * g.heads + head]);
 #pragma unroll
-    for (int g = 0; g < kMaxG; ++g) {
-        m[g] = -INFINITY;
-        l[g] = 0.0f;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float acc[kMaxD / 32], l = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kMaxD / 32; ++i) {
-            o[g][i] = qv[g][i] = 0.0f;
-            if (g < G && i < D / 32) {
-                const int64_t at = row * a.q_tok + (static_cast<int64_t>(h) * G + g) * a.q_head + lane + 32 * i;
-                qv[g][i] = QT == FATHOM_KEYS_F32 ? static_cast<const float*>(a.q)[at]
-                                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at]);
-            }
-        }
-    }
-    for (int64_t i0 = warp; i0 < keys; i0 += kSimpleWarps) {
-        int64_t pos = i0;
-        if (UNION) {
-            pos = a.uni[h * a.M + i0];
-            if (pos < 0 || pos >= a.n) continue;
-        }
-        const int page = kv_page(a.c, table, a.w.table_pages, pos);
-        if (page < 0) continue;
-        const int token = static_cast<int>(pos & (a.c.page_tokens - 1));
-        const int64_t at = kv_off(a.c, page, h, token);
-        const int64_t sat = FMT == FATHOM_KV_BF16 ? 0 : kv_scale_off(a.c, page, h, token);
-        float kx[kMaxD / 32], vx[kMaxD / 32];
+    for (int i = 0; i < kMaxD / 32; ++i) acc[i] = 0.0f;
+    if (top != -INFINITY) {
+#pragma unroll 4
+        for (int s = warp; s < n; s += kJoinWarps) {
+            const int64_t at = s * g.heads + head;
+            const float f = exp2_fast(g.pm[at] - top);
+            l += g.pl[at] * f;
 #pragma unroll
-        for (int i = 0; i < kMaxD / 32; ++i) {
-            kx[i] = vx[i] = 0.0f;
-            if (i < D / 32) {
-                kx[i] = kv_value<FMT>(a.c.k + at, lane + 32 * i, FMT == FATHOM_KV_BF16 ? 0 : a.c.ks[sat + i]);
-                vx[i] = kv_value<FMT>(a.c.v + at, lane + 32 * i, FMT == FATHOM_KV_BF16 ? 0 : a.c.vs[sat + i]);
-            }
-        }
-#pragma unroll
-        for (int g = 0; g < kMaxG; ++g) {
-            if (g >= G) break;
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kMaxD / 32; ++i) s = fmaf(qv[g][i], kx[i], s);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            s *= a.scale;
-            const float top = fmaxf(m[g], s);
-            const float f = m[g] == -INFINITY ? 0.0f : expf(m[g] - top), p = expf(s - top);
-            m[g] = top;
-            l[g] = l[g] * f + p;
-#pragma unroll
-            for (int i = 0; i < kMaxD / 32; ++i) o[g][i] = o[g][i] * f + p * vx[i];
+            for (int i = 0; i < kMaxD / 32; ++i)
+                if (i < D / 32) acc[i] = fmaf(g.po[at * D + lane + 32 * i], f, acc[i]);
         }
     }
-    float* sm_m = sm + kSimpleWarps * G * D;
-    float* sm_l = sm_m + kSimpleWarps * G;
 #pragma unroll
-    for (int g = 0; g < kMaxG; ++g) {
-        if (g >= G) break;
-#pragma unroll
-        for (int i = 0; i < kMaxD / 32; ++i)
-            if (i < D / 32) sm[(warp * G + g) * D + lane + 32 * i] = o[g][i];
-        if (lane == 0) {
-            sm_m[warp * G + g] = m[g];
-            sm_l[warp * G + g] = l[g];
-        }
-    }
+    for (int i = 0; i < kMaxD / 32; ++i)
+        if (i < D / 32) part[warp][lane + 32 * i] = acc[i];
+    if (lane == 0) part_l[warp] = l;
     __syncthreads();
-    for (int e = threadIdx.x; e < G * D; e += blockDim.x) {
-        const int g = e / D;
-        float top = -INFINITY, sum = 0.0f, val = 0.0f;
-        for (int w = 0; w < kSimpleWarps; ++w) top = fmaxf(top, sm_m[w * G + g]);
-        if (top != -INFINITY)
-            for (int w = 0; w < kSimpleWarps; ++w) {
-                const float f = sm_m[w * G + g] == -INFINITY ? 0.0f : expf(sm_m[w * G + g] - top);
-                sum += sm_l[w * G + g] * f;
-                val += sm[(w * G + g) * D + e % D] * f;
-            }
-        const float r = top == -INFINITY ? 0.0f : val / sum;
-        const int64_t to = (static_cast<int64_t>(row) * a.c.H + h) * G * D + e;
-        if (QT == FATHOM_KEYS_F32) static_cast<float*>(a.out)[to] = r;
-        else static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16(r);
+    for (int d = threadIdx.x; d < D; d += kJoinThreads) {
+        float x = 0.0f, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            x += part[w][d];
+            sum += part_l[w];
+        }
+        const float y = top == -INFINITY ? 0.0f : x / sum;
+        if (QT == FATHOM_KEYS_F32) static_cast<float*>(a.out)[head * D + d] = y;
+        else static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16(y);
     }
 }
 
-template <int FMT, int QT, bool UNION>
-int launch_simple(const KvAttend& a, int rows, cudaStream_t stream)
+int launch_join(const KvRowsArgs& g, int q_dtype, cudaStream_t stream)
 {
-    const size_t smem = sizeof(float) * kSimpleWarps * a.G * (a.c.D + 2);
-    const int st = ensure_dynamic_smem(reinterpret_cast<const void*>(kv_attend_kernel<FMT, QT, UNION>), smem);
-    if (st) return st;
-    kv_attend_kernel<FMT, QT, UNION><<<dim3(rows, a.c.H), 32 * kSimpleWarps, smem, stream>>>(a);
-    return launch_status();
-}
-
-template <int FMT>
-int launch_attend_f(const KvAttend& a, int q_dtype, bool uni, cudaStream_t stream)
-{
-    if (uni) return launch_simple<FMT, FATHOM_KEYS_F32, true>(a, 1, stream);
-    if (q_dtype == FATHOM_KEYS_F32) return launch_simple<FMT, FATHOM_KEYS_F32, false>(a, a.w.rows, stream);
-    return launch_simple<FMT, FATHOM_KEYS_BF16, false>(a, a.w.rows, stream);
+    const dim3 grid(static_cast<unsigned>(g.a.uni ? 1 : g.a.w.rows), static_cast<unsigned>(g.a.c.H * g.a.G));
+    if (q_dtype == FATHOM_KEYS_F32) return launch_pdl(kv_join_kernel<FATHOM_KEYS_F32>, grid, kJoinThreads, 0, stream, g);
+    return launch_pdl(kv_join_kernel<FATHOM_KEYS_BF16>, grid, kJoinThreads, 0, stream, g);
 }
 
 }  // namespace
 
-size_t paged_attention_workspace_bytes(int, int, int, int64_t, int, int64_t, int64_t, int) { return 0; }
-size_t paged_union_attention_workspace_bytes(int64_t, int, int, int64_t) { return 0; }
-
-int launch_paged_attention(const KvAttend& a, int format, int q_dtype, void*, cudaStream_t stream)
+size_t paged_attention_workspace_bytes(int H, int G, int D, int64_t rows, int B, int64_t max_new, int64_t max_len, int)
 {
-    const bool uni = a.uni != nullptr;
-    switch (format) {
-        case FATHOM_KV_BF16: return launch_attend_f<FATHOM_KV_BF16>(a, q_dtype, uni, stream);
-        case FATHOM_KV_INT8: return launch_attend_f<FATHOM_KV_INT8>(a, q_dtype, uni, stream);
-        default: return launch_attend_f<FATHOM_KV_E4M3>(a, q_dtype, uni, stream);
+    const KvSplit s = rows_split(H, G, D, B, std::min(max_new, rows), max_len);
+    return parts_bytes(rows * H * G, s.splits, D);
+}
+
+size_t paged_union_attention_workspace_bytes(int64_t H, int G, int D, int64_t M)
+{
+    return parts_bytes(H * G, union_split(H, M).splits, D);
+}
+
+int launch_paged_attention(const KvAttend& a, int format, int q_dtype, void* ws, cudaStream_t stream)
+{
+    KvRowsArgs g{};
+    g.a = a;
+    g.s = a.uni ? union_split(a.c.H, a.M) : rows_split(a.c.H, a.G, a.c.D, a.w.B, a.max_new, a.max_len);
+    g.heads = static_cast<int64_t>(a.w.rows) * a.c.H * a.G;
+    unsigned char* base = static_cast<unsigned char*>(ws);
+    if (g.s.splits > 1) {
+        g.po = reinterpret_cast<float*>(base);
+        g.pm = reinterpret_cast<float*>(base + up256(sizeof(float) * g.s.splits * g.heads * a.c.D));
+        g.pl = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(g.pm) + up256(sizeof(float) * g.s.splits * g.heads));
     }
+    const int st = format == FATHOM_KV_BF16 ? launch_rows_bf16(g, q_dtype, stream)
+                   : format == FATHOM_KV_INT8 ? launch_rows_int8(g, q_dtype, stream)
+                                              : launch_rows_e4m3(g, q_dtype, stream);
+    if (st || g.s.splits <= 1) return st;
+    return launch_join(g, q_dtype, stream);
 }
 
 }  // namespace fathom
