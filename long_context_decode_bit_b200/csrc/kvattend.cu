@@ -2,7 +2,7 @@
 // up, and the joining of its stretches.
 #include <algorithm>
 
-#include "kvrows.cuh"
+#include "kvchunk.cuh"
 
 namespace fathom {
 
@@ -14,14 +14,38 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 
 int64_t round_up(int64_t x, int64_t to) { return ceil_div(x, to) * to; }
 
-// Rows of 8*nt query rows by stretches of tokens.  A CTA's four warps want
+// Tiles of kChunkRows query rows, one CTA to an SM.  The cut into stretches
+// that ends soonest: waves of CTAs times a stretch's tiles of tokens (and
+// about three tiles' time to start and end a CTA).
+KvSplit chunk_split(int H, int B, int64_t qrows, int64_t max_len)
+{
+    KvSplit s{};
+    s.tile_rows = kChunkRows;
+    s.row_tiles = static_cast<int32_t>(ceil_div(qrows, kChunkRows));
+    const int64_t items = static_cast<int64_t>(B) * H * s.row_tiles, tiles = std::max<int64_t>(1, ceil_div(max_len, kChunkKeys));
+    int64_t best = 0, each = tiles;
+    for (int64_t n = 1; n <= 32 && n <= tiles; ++n) {
+        const int64_t len = ceil_div(tiles, n), cost = ceil_div(items * n, kSms) * (len + 3 + (n > 1 ? 1 : 0));
+        if (n == 1 || cost < best) {
+            best = cost;
+            each = len;
+        }
+    }
+    s.chunk = static_cast<int32_t>(each * kChunkKeys);
+    s.splits = static_cast<int32_t>(ceil_div(tiles, each));
+    return s;
+}
+
+// Tiles of 8*nt query rows by stretches of tokens.  A CTA's four warps want
 // 64 tokens at least each; four CTAs fit an SM.
-KvSplit rows_split(int H, int G, int D, int B, int64_t max_new, int64_t max_len)
+KvSplit rows_split(int H, int G, int D, int B, int64_t max_new, int64_t max_len, int q_dtype)
 {
     KvSplit s{};
     const int64_t qrows = max_new * G;
+    if (q_dtype == FATHOM_KEYS_BF16 && (D == 64 || D == 128) && qrows > 64) return chunk_split(H, B, qrows, max_len);
     s.nt = qrows <= 8 ? 1 : (D <= 128 ? 4 : 2);
-    s.row_tiles = static_cast<int32_t>(ceil_div(qrows, 8 * s.nt));
+    s.tile_rows = 8 * s.nt;
+    s.row_tiles = static_cast<int32_t>(ceil_div(qrows, s.tile_rows));
     const int64_t items = static_cast<int64_t>(B) * H * s.row_tiles;
     // One session: its stretches are equal, one wave of CTAs.  Several of uneven
     // lengths: shorter stretches, so that the longest session does not end alone.
@@ -36,7 +60,7 @@ KvSplit rows_split(int H, int G, int D, int B, int64_t max_new, int64_t max_len)
 
 KvSplit union_split(int64_t H, int64_t M)
 {
-    KvSplit s{1, 1, 1, 0};
+    KvSplit s{1, 8, 1, 1, 0};
     const int64_t splits = std::max<int64_t>(1, 4 * kSms / H);
     s.chunk = static_cast<int32_t>(std::max<int64_t>(round_up(ceil_div(M, splits), 64), 64));
     s.splits = static_cast<int32_t>(ceil_div(M, s.chunk));
@@ -73,8 +97,8 @@ kv_join_kernel(const KvRowsArgs g)
         const KvSpan sp = kv_span(a, b);
         const int qr = static_cast<int>(row - sp.first) * a.G + blockIdx.y % a.G;
         if (row - sp.first >= sp.rows) return;
-        const int r0 = qr / (8 * g.s.nt) * 8 * g.s.nt;
-        n = static_cast<int>(ceil_div(kv_tile_keys(a, sp, r0, 8 * g.s.nt), g.s.chunk));
+        const int r0 = qr / g.s.tile_rows * g.s.tile_rows;
+        n = static_cast<int>(ceil_div(kv_tile_keys(a, sp, r0, g.s.tile_rows), g.s.chunk));
     }
     float top = -INFINITY;
     for (int s = lane; s < n; s += 32) top = fmaxf(top, g.pm[s * g.heads + head]);
@@ -83,16 +107,15 @@ kv_join_kernel(const KvRowsArgs g)
     float acc[kMaxD / 32], l = 0.0f;
 #pragma unroll
     for (int i = 0; i < kMaxD / 32; ++i) acc[i] = 0.0f;
-    if (top != -INFINITY) {
+    const float low = top == -INFINITY ? 0.0f : top;
 #pragma unroll 4
-        for (int s = warp; s < n; s += kJoinWarps) {
-            const int64_t at = s * g.heads + head;
-            const float f = exp2_fast(g.pm[at] - top);
-            l += g.pl[at] * f;
+    for (int s = warp; s < n; s += kJoinWarps) {
+        const int64_t at = s * g.heads + head;
+        const float f = exp2_fast(g.pm[at] - low);
+        l += g.pl[at] * f;
 #pragma unroll
-            for (int i = 0; i < kMaxD / 32; ++i)
-                if (i < D / 32) acc[i] = fmaf(g.po[at * D + lane + 32 * i], f, acc[i]);
-        }
+        for (int i = 0; i < kMaxD / 32; ++i)
+            if (i < D / 32) acc[i] = fmaf(g.po[at * D + lane + 32 * i], f, acc[i]);
     }
 #pragma unroll
     for (int i = 0; i < kMaxD / 32; ++i)
@@ -106,7 +129,7 @@ kv_join_kernel(const KvRowsArgs g)
             x += part[w][d];
             sum += part_l[w];
         }
-        const float y = top == -INFINITY ? 0.0f : x / sum;
+        const float y = sum == 0.0f ? 0.0f : x / sum;   // no token was seen (NaN scores make the sum NaN)
         if (QT == FATHOM_KEYS_F32) static_cast<float*>(a.out)[head * D + d] = y;
         else static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16(y);
     }
@@ -121,9 +144,10 @@ int launch_join(const KvRowsArgs& g, int q_dtype, cudaStream_t stream)
 
 }  // namespace
 
-size_t paged_attention_workspace_bytes(int H, int G, int D, int64_t rows, int B, int64_t max_new, int64_t max_len, int)
+size_t paged_attention_workspace_bytes(int H, int G, int D, int64_t rows, int B, int64_t max_new, int64_t max_len,
+                                       int q_dtype)
 {
-    const KvSplit s = rows_split(H, G, D, B, std::min(max_new, rows), max_len);
+    const KvSplit s = rows_split(H, G, D, B, std::min(max_new, rows), max_len, q_dtype);
     return parts_bytes(rows * H * G, s.splits, D);
 }
 
@@ -136,7 +160,7 @@ int launch_paged_attention(const KvAttend& a, int format, int q_dtype, void* ws,
 {
     KvRowsArgs g{};
     g.a = a;
-    g.s = a.uni ? union_split(a.c.H, a.M) : rows_split(a.c.H, a.G, a.c.D, a.w.B, a.max_new, a.max_len);
+    g.s = a.uni ? union_split(a.c.H, a.M) : rows_split(a.c.H, a.G, a.c.D, a.w.B, a.max_new, a.max_len, q_dtype);
     g.heads = static_cast<int64_t>(a.w.rows) * a.c.H * a.G;
     unsigned char* base = static_cast<unsigned char*>(ws);
     if (g.s.splits > 1) {
@@ -144,7 +168,8 @@ int launch_paged_attention(const KvAttend& a, int format, int q_dtype, void* ws,
         g.pm = reinterpret_cast<float*>(base + up256(sizeof(float) * g.s.splits * g.heads * a.c.D));
         g.pl = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(g.pm) + up256(sizeof(float) * g.s.splits * g.heads));
     }
-    const int st = format == FATHOM_KV_BF16 ? launch_rows_bf16(g, q_dtype, stream)
+    const int st = g.s.nt == 0                 ? launch_chunk(g, format, stream)
+                   : format == FATHOM_KV_BF16 ? launch_rows_bf16(g, q_dtype, stream)
                    : format == FATHOM_KV_INT8 ? launch_rows_int8(g, q_dtype, stream)
                                               : launch_rows_e4m3(g, q_dtype, stream);
     if (st || g.s.splits <= 1) return st;

@@ -1,0 +1,591 @@
+// Attention of prompt chunks over the paged cache on the tensor memory's
+// matrix units (tcgen05): bf16 queries, 64 or 128 channels.
+//
+// A CTA takes 256 query rows (a row is one head of one token; the G heads of
+// a group lie next to each other, so they share every cached byte) as two
+// tiles of 128, and the tokens of one stretch in tiles of 128.  Per tile of
+// tokens and of rows
+//   S [128 x 128] = Q K^T  (both in shared memory, accumulators in tensor memory),
+//   P = 2^(S scale log2 e - m), l += row sums,
+//   O [128 x D] += P V     (P in tensor memory over S, V in shared memory).
+// Roles: warps 0-3 and 4-7 are the softmax of the two row tiles, a thread to
+// a row; warps 8-11 bring K and V; one thread of warp 12 issues the products.
+// The row tiles take turns: while one's softmax runs, the other's products do.
+//
+// Both operands are kept with 64 channels (128 bytes) to a row and the
+// 128-byte swizzle, K read along the channels and V along the tokens from the
+// same layout.  16-bit pages are copied there by cp.async, 16 bytes a thread,
+// zeros for tokens that are not there; 8-bit pages are decoded to bf16 on the
+// way (once for 256 query rows), their next tile already in registers.
+//
+// The running maximum m of a row is raised only when it grew by more than
+// 2^8 (P and l then stay below 2^8 times what the true maximum gives, far
+// inside bf16's and fp32's range), so O is rarely touched between products.
+// P enters the product in bf16 (relative 2^-9 to a weight); l sums the
+// unrounded weights in fp32.
+//
+// Every wait on a barrier has an iteration limit; a role whose wait runs out
+// sets the fault word and leaves its loop, and the CTA frees its tensor memory.
+#pragma once
+
+#include "kvrows.cuh"
+#include "ring.cuh"
+
+namespace fathom {
+
+constexpr int kChunkThreads = 512;
+constexpr int kChunkRows = 256;   // query rows of a CTA
+constexpr int kChunkKeys = 128;   // tokens of a tile
+// Registers a thread of each role keeps; their sum is the launch's 4 x 128.
+constexpr int kRegsSoftmax = 192, kRegsLoad = 80, kRegsIssue = 48;
+static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 512, "more registers than the block has");
+
+template <int D>
+struct ChunkShape {
+    static constexpr int DB = D / 64;                             // 64-channel blocks of a row
+    static constexpr int TILE = kChunkKeys * 128 * DB;            // bytes of 128 rows
+    static constexpr int STAGES = D == 128 ? 5 : 8;               // tiles of K or V held
+    static constexpr int QB = 2 * TILE;
+    static constexpr size_t BARS = QB + static_cast<size_t>(STAGES) * TILE;
+    static constexpr size_t SMEM = BARS + 256 + 1024;             // the base is moved up to a multiple of 1024
+};
+
+// ---- tensor memory and its products (cta_group::1)
+
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_at, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_at), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(at), "r"(cols));
+}
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
+// `bar` gets one arrival when every product issued so far by this thread is done.
+__device__ __forceinline__ void tc_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+
+// 32 or 16 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float* x)
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float* x)
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Shared-memory operand in 128-byte rows with the 128-byte swizzle: groups of
+// 8 rows are 1024 bytes apart; `lbo` is the distance of 64-channel blocks
+// where the product runs along the rows (V).
+__device__ __forceinline__ uint64_t tc_operand(uint32_t smem_at, uint32_t lbo)
+{
+    return (static_cast<uint64_t>(2) << 61) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+           (static_cast<uint64_t>(lbo >> 4) << 16) | ((smem_at & 0x3ffff) >> 4);
+}
+
+// bf16 x bf16 -> fp32, 128 rows, N columns; `along_rows`: B is stored [k][n].
+__host__ __device__ constexpr uint32_t tc_shape(int N, bool along_rows)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (along_rows ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
+// ---- pairs of fp32
+
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b)   // x = x a + b, y = y a + b
+{
+    asm("{\n .reg .b64 u, v, w;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %2};\n mov.b64 w, {%3, %3};\n fma.rn.f32x2 u, u, v, w;\n"
+        " mov.b64 {%0, %1}, u;\n}\n"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b)   // x += a, y += b
+{
+    asm("{\n .reg .b64 u, v;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %3};\n add.rn.f32x2 u, u, v;\n mov.b64 {%0, %1}, u;\n}\n"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+
+// ---- bringing K and V
+
+// 16-byte piece `piece` (of D/8) of row `row` of a tile.
+__device__ __forceinline__ uint32_t tile_at(int row, int piece)
+{
+    return (piece >> 3) * (kChunkKeys * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t at, uint4 x)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+
+__device__ __forceinline__ void cp_async16_to(uint32_t at, const void* gmem, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(at), "l"(gmem), "r"(bytes) : "memory");
+}
+
+// Page of the 16 tokens from `at` + 16*lane (lanes 0..7), -1 for none of this stretch's.
+__device__ __forceinline__ int chunk_page(const KvCache& c, const int32_t* table, int table_pages, int at, int end, int lane)
+{
+    const int pos = at + 16 * lane;
+    return lane < 8 && pos < end ? kv_page(c, table, table_pages, pos) : -1;
+}
+
+// The whole 128-token tiles of K and V from `begin` on, in the order K0 V0 K1 V1 ..., into the ring.
+template <int D, int FMT>
+__device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* table, int table_pages, int h, int begin, int end,
+                                           uint32_t ring, uint32_t full, uint32_t empty)
+{
+    using S = ChunkShape<D>;
+    const int t = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const int tiles = (end - begin + kChunkKeys - 1) / kChunkKeys;
+    bool ok = true;
+    int page = chunk_page(c, table, table_pages, begin, end, lane), next = -1;
+    if constexpr (FMT == FATHOM_KV_BF16) {
+        constexpr int PIECES = D / 8, ROWS = 128 / PIECES;   // rows of a pass
+        constexpr int AHEAD = S::STAGES - 2;                 // stages that may be on their way
+        const int piece = t % PIECES, r0 = t / PIECES;
+        int i = 0;
+        for (int j = 0; j < tiles && ok; ++j) {
+            const int at = begin + j * kChunkKeys;
+            next = chunk_page(c, table, table_pages, at + kChunkKeys, end, lane);
+            for (int s = 0; s < 2; ++s, ++i) {
+                const int st = i % S::STAGES;
+                ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((i / S::STAGES) & 1) ^ 1));
+                if (!ok) break;
+                const unsigned char* data = s ? c.v : c.k;
+#pragma unroll
+                for (int p = 0; p < 128 / ROWS; ++p) {
+                    const int row = r0 + p * ROWS;
+                    const int pg = __shfl_sync(0xffffffffu, page, row >> 4);
+                    const bool live = pg >= 0 && at + row < end;
+                    const unsigned char* from =
+                        live ? data + kv_off(c, pg, h, (at + row) & (c.page_tokens - 1)) + piece * 16 : data;
+                    cp_async16_to(ring + st * S::TILE + tile_at(row, piece), from, live ? 16 : 0);
+                }
+                asm volatile("cp.async.commit_group;\n" ::: "memory");
+                if (i >= AHEAD) {
+                    asm volatile("cp.async.wait_group %0;\n" ::"n"(AHEAD) : "memory");
+                    fence_async_smem();
+                    mbar_arrive(full + 8 * ((i - AHEAD) % S::STAGES));
+                }
+            }
+            page = next;
+        }
+        cp_async_wait_all();
+        fence_async_smem();
+        if (ok)
+            for (int k = max(0, i - AHEAD); k < i; ++k) mbar_arrive(full + 8 * (k % S::STAGES));
+    } else {
+        constexpr int PIECES = D / 16, ROWS = 128 / PIECES, N = 128 / ROWS;   // 16 codes to a piece
+        const int piece = t % PIECES, r0 = t / PIECES;
+        uint4 raw[N];
+        uint32_t pw[N];
+        auto fetch = [&](int at, bool v) {
+            const unsigned char* data = v ? c.v : c.k;
+            const unsigned char* sc = v ? c.vs : c.ks;
+#pragma unroll
+            for (int p = 0; p < N; ++p) {
+                const int row = r0 + p * ROWS;
+                const int pg = __shfl_sync(0xffffffffu, page, row >> 4);
+                raw[p] = make_uint4(0, 0, 0, 0);
+                pw[p] = 0;
+                if (pg >= 0 && at + row < end) {
+                    const int tok = (at + row) & (c.page_tokens - 1);
+                    raw[p] = __ldg(reinterpret_cast<const uint4*>(data + kv_off(c, pg, h, tok) + piece * 16));
+                    pw[p] = __ldg(sc + kv_scale_off(c, pg, h, tok) + (piece >> 1));
+                }
+            }
+        };
+        int i = 0;
+        if (tiles > 0) fetch(begin, false);
+        for (int j = 0; j < tiles && ok; ++j) {
+            const int at = begin + j * kChunkKeys;
+            next = chunk_page(c, table, table_pages, at + kChunkKeys, end, lane);
+#pragma unroll
+            for (int s = 0; s < 2; ++s, ++i) {
+                const int st = i % S::STAGES;
+                ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((i / S::STAGES) & 1) ^ 1));
+                if (!ok) break;
+#pragma unroll
+                for (int p = 0; p < N; ++p) {
+                    const int row = r0 + p * ROWS;
+                    const uint32_t f = pow_bits<FMT>(pw[p]) * 0x10001u;
+                    const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
+                    uint4 o[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        o[k] = make_uint4(decode2<FMT, 0, 1>(w[2 * k], w[2 * k], f), decode2<FMT, 2, 3>(w[2 * k], w[2 * k], f),
+                                          decode2<FMT, 0, 1>(w[2 * k + 1], w[2 * k + 1], f),
+                                          decode2<FMT, 2, 3>(w[2 * k + 1], w[2 * k + 1], f));
+                    // half of the threads store their second piece first: 8 threads then fill all banks once
+                    const int first = (piece >> 2) & 1;
+                    const uint32_t to = ring + st * S::TILE;
+                    st_shared16(to + tile_at(row, 2 * piece + first), first ? o[1] : o[0]);
+                    st_shared16(to + tile_at(row, 2 * piece + 1 - first), first ? o[0] : o[1]);
+                }
+                if (s == 0) {
+                    fetch(at, true);
+                } else {
+                    page = next;
+                    if (j + 1 < tiles) fetch(at + kChunkKeys, false);
+                }
+                fence_async_smem();
+                mbar_arrive(full + 8 * st);
+            }
+        }
+    }
+    return ok;
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
+{
+    using S = ChunkShape<D>;
+    constexpr int ST = S::STAGES;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* base = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const uint32_t q_s = smem_addr(base), ring = q_s + S::QB, bars = q_s + static_cast<uint32_t>(S::BARS);
+    const uint32_t full = bars, empty = bars + 8 * ST, s_full = bars + 16 * ST, p_full = s_full + 16, o_full = p_full + 16,
+                   q_full = o_full + 16, drain = q_full + 8, tmem_slot = drain + 8;
+    static_assert(16 * ST + 16 * 3 + 8 * 2 + 4 <= 256, "barriers fit their space");
+
+    const KvAttend& a = g.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.y, b = blockIdx.z, G = a.G;
+    // Later rows see more tokens: they start first.
+    const int tile = g.s.row_tiles - 1 - static_cast<int>(blockIdx.x % g.s.row_tiles), split = blockIdx.x / g.s.row_tiles;
+    const int r0 = tile * kChunkRows;
+    const KvSpan sp = kv_span(a, b);
+    const int nrows = sp.rows * G;
+    if (r0 >= nrows) return;
+    const int keys = kv_tile_keys(a, sp, r0, kChunkRows);
+    const int begin = split * g.s.chunk, end = min(keys, begin + g.s.chunk);
+    if (begin >= keys && split > 0) return;   // the join knows
+    const int tiles = (max(end - begin, 0) + kChunkKeys - 1) / kChunkKeys;
+    const bool two = r0 + 128 < nrows;        // the second row tile has rows
+    const int32_t* table = a.w.table + b * a.w.table_stride;
+
+    if (warp == 12) {
+        tmem_alloc(tmem_slot, 512);
+        if (lane == 0) {
+            for (int i = 0; i < ST; ++i) {
+                mbar_init(full + 8 * i, 128);
+                mbar_init(empty + 8 * i, 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(s_full + 8 * i, 1);
+                mbar_init(p_full + 8 * i, 128);
+                mbar_init(o_full + 8 * i, 1);
+            }
+            mbar_init(q_full, 128);
+            mbar_init(drain, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        }
+        tc_before();
+    }
+    __syncthreads();
+    tc_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(tmem) : "r"(tmem_slot));
+
+    if (warp >= 12) {
+        regs_down<kRegsIssue>();
+        if (warp == 12 && lane == 0 && tiles > 0) {
+            constexpr uint32_t shape_s = tc_shape(kChunkKeys, false), shape_o = tc_shape(D, true);
+            auto scores = [&](int t, int st) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * (kChunkKeys * 128) + (ks & 3) * 32;
+                    tc_mma_ss(tmem + 128 * t, tc_operand(q_s + t * S::TILE + off, 0), tc_operand(ring + st * S::TILE + off, 0),
+                              shape_s, ks > 0);
+                }
+                tc_commit(s_full + 8 * t);
+            };
+            auto values = [&](int t, int st, bool add) {
+#pragma unroll
+                for (int ks = 0; ks < kChunkKeys / 16; ++ks)
+                    tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * ks,
+                              tc_operand(ring + st * S::TILE + ks * 2048, kChunkKeys * 128), shape_o, add || ks > 0);
+            };
+            const int nt = two ? 2 : 1;
+            bool ok = mbar_wait(q_full, 0) && mbar_wait(full, 0);
+            if (ok) {
+                tc_after();
+                for (int t = 0; t < nt; ++t) scores(t, 0);
+                tc_commit(empty);
+            }
+            for (int j = 0; j < tiles && ok; ++j) {
+                const int iv = 2 * j + 1, ik = iv + 1;
+                const bool more = j + 1 < tiles;
+                ok = mbar_wait(full + 8 * (iv % ST), (iv / ST) & 1);
+                for (int t = 0; t < nt && ok; ++t) {
+                    ok = mbar_wait(p_full + 8 * t, j & 1);
+                    if (!ok) break;
+                    tc_after();
+                    values(t, iv % ST, j > 0);
+                    if (!more) tc_commit(o_full + 8 * t);
+                    if (t == nt - 1) tc_commit(empty + 8 * (iv % ST));
+                    if (more) {
+                        if (t == 0) ok = mbar_wait(full + 8 * (ik % ST), (ik / ST) & 1);
+                        if (!ok) break;
+                        scores(t, ik % ST);
+                    }
+                }
+                if (ok && more) tc_commit(empty + 8 * (ik % ST));
+            }
+            if (!ok) atomicOr(fault, kFaultTimeout);
+            // Nothing is on its way in tensor memory when it is freed.
+            tc_commit(drain);
+            if (!mbar_wait(drain, 0)) atomicOr(fault, kFaultTimeout);
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        regs_down<kRegsLoad>();
+        {
+            constexpr int PIECES = D / 8, ROWS = 128 / PIECES;
+            const int t = threadIdx.x & 127, piece = t % PIECES, at_row = t / PIECES;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+            const bool vec = ((reinterpret_cast<uintptr_t>(q) & 15) | (a.q_tok & 7) | (a.q_head & 7)) == 0;
+            const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // the softmax uses |scale|
+            for (int row = at_row; row < kChunkRows; row += ROWS) {
+                const int qr = r0 + row;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (qr < nrows) {
+                    const __nv_bfloat16* from =
+                        q + (sp.first + qr / G) * a.q_tok + (static_cast<int64_t>(h) * G + qr % G) * a.q_head + piece * 8;
+                    if (vec) {
+                        x = __ldg(reinterpret_cast<const uint4*>(from));
+                    } else {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = __bfloat16_as_ushort(from[2 * i]) |
+                                   static_cast<uint32_t>(__bfloat16_as_ushort(from[2 * i + 1])) << 16;
+                        x = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    x.x ^= flip;
+                    x.y ^= flip;
+                    x.z ^= flip;
+                    x.w ^= flip;
+                }
+                st_shared16(q_s + (row >> 7) * S::TILE + tile_at(row & 127, piece), x);
+            }
+            fence_async_smem();
+            mbar_arrive(q_full);
+        }
+        if (!chunk_load<D, FMT>(a.c, table, a.w.table_pages, h, begin, end, ring, full, empty)) atomicOr(fault, kFaultTimeout);
+    } else {
+        regs_up<kRegsSoftmax>();
+        const int t = warp >> 2;
+        const int qr = r0 + threadIdx.x;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + 128 * t;
+        // Tokens before `mine` are seen by this thread's row (a row that is not there: all).
+        const int mine = a.causal && qr < nrows ? min(end, sp.pos0 + qr / G + 1) : end;
+        // No smaller than the least normal number: -inf times it stays -inf, and 2^(x 1e-38) is 1.
+        const float log2s = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        if (t == 0 || two) {
+            int page = chunk_page(a.c, table, a.w.table_pages, begin, end, lane);
+            for (int j = 0; j < tiles; ++j) {
+                const int at = begin + j * kChunkKeys;
+                const uint32_t live = __ballot_sync(0xffffffffu, page >= 0);
+                page = chunk_page(a.c, table, a.w.table_pages, at + kChunkKeys, end, lane);
+                ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * t, j & 1));
+                if (!ok) break;
+                tc_after();
+                float s[kChunkKeys];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
+                tmem_ld_wait();
+                const int lim = mine - at;
+                if (!__all_sync(0xffffffffu, lim >= kChunkKeys) || live != 0xff) {
+#pragma unroll
+                    for (int i = 0; i < kChunkKeys; ++i)
+                        if (i >= lim || !((live >> (i >> 4)) & 1)) s[i] = -INFINITY;
+                }
+                float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int i = 4; i < kChunkKeys; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        top[k] = i + 4 + k < kChunkKeys ? fmaxf(fmaxf(top[k], s[i + k]), s[i + 4 + k]) : fmaxf(top[k], s[i + k]);
+                const float peak = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * log2s);
+                if (__any_sync(0xffffffffu, peak > m + 8.0f)) {
+                    const float f = exp2_fast(m - (peak == -INFINITY ? 0.0f : peak));
+                    l *= f;
+                    m = peak;
+                    if (j > 0) {   // the product before is done: this tile's scores came after it
+#pragma unroll
+                        for (int i = 0; i < D; i += 16) {
+                            float o[16];
+                            tmem_ld16(o_at + i, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] *= f;
+                            tmem_st16(o_at + i, reinterpret_cast<const uint32_t*>(o));
+                        }
+                    }
+                }
+                const float low = m == -INFINITY ? 0.0f : -m;
+                float sum[4] = {l, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int part = 0; part < 4; ++part) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x = s[32 * part + 2 * i], y = s[32 * part + 2 * i + 1];
+                        fma2(x, y, log2s, low);
+                        x = exp2_fast(x);
+                        y = exp2_fast(y);
+                        add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], x, y);
+                        p[i] = bf16x2(x, y);
+                    }
+                    tmem_st16(s_at + 16 * part, p);
+                }
+                l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_before();
+                mbar_arrive(p_full + 8 * t);
+            }
+            if (ok && tiles > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(o_full + 8 * t, 0));
+                tc_after();
+            }
+            if (!ok) {
+                if (lane == 0) atomicOr(fault, kFaultTimeout);
+            } else {
+                const int64_t head = ((sp.first + qr / G) * a.c.H + h) * G + qr % G;
+                const bool parts = g.s.splits > 1;
+                const float f = parts ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f);
+                const int64_t at_p = split * g.heads + head;
+                const bool nothing = l == 0.0f;   // no token was seen (NaN scores make l NaN)
+#pragma unroll
+                for (int i = 0; i < D; i += 32) {
+                    float o[32];
+                    if (tiles > 0) {
+                        tmem_ld32(o_at + i, o);
+                        tmem_ld_wait();
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = nothing ? 0.0f : o[k] * f;
+                    if (qr < nrows) {
+                        if (parts) {
+                            float4* to = reinterpret_cast<float4*>(g.po + at_p * D + i);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        } else {
+                            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + head * D + i;
+                            if ((reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    reinterpret_cast<uint4*>(to)[k] =
+                                        make_uint4(bf16x2(o[8 * k], o[8 * k + 1]), bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                                   bf16x2(o[8 * k + 4], o[8 * k + 5]), bf16x2(o[8 * k + 6], o[8 * k + 7]));
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) to[k] = __float2bfloat16(o[k]);
+                            }
+                        }
+                    }
+                }
+                if (parts && qr < nrows) {
+                    g.pm[at_p] = m;
+                    g.pl[at_p] = l;
+                }
+            }
+        }
+        tc_before();
+    }
+    __syncthreads();
+    if (warp == 12) {
+        tc_after();
+        tmem_free(tmem, 512);
+    }
+    pdl_launch_dependents();
+}
+
+template <int D, int FMT>
+int launch_chunk_t(const KvRowsArgs& g, cudaStream_t stream)
+{
+    using S = ChunkShape<D>;
+    const void* f = reinterpret_cast<const void*>(kv_chunk_kernel<D, FMT>);
+    // The roles' registers must add up to no more than the block is launched with, or the softmax waits for ever.
+    static const int launch_regs = [f] {
+        cudaFuncAttributes attr;
+        return cudaFuncGetAttributes(&attr, f) == cudaSuccess ? attr.numRegs : 0;
+    }();
+    if (4 * launch_regs < 2 * kRegsSoftmax + kRegsLoad + kRegsIssue) return FATHOM_ERR_UNSUPPORTED;
+    int32_t* fault = nullptr;
+    int st = device_fault_word(&fault);
+    if (st) return st;
+    st = ensure_dynamic_smem(f, S::SMEM);
+    if (st) return st;
+    const dim3 grid(static_cast<unsigned>(g.s.splits) * g.s.row_tiles, static_cast<unsigned>(g.a.c.H),
+                    static_cast<unsigned>(g.a.w.B));
+    kv_chunk_kernel<D, FMT><<<grid, kChunkThreads, S::SMEM, stream>>>(g, fault);
+    return launch_status();
+}
+
+// kvchunk.cu: chunks of bf16 queries over caches of 64 or 128 channels.
+int launch_chunk(const KvRowsArgs& g, int format, cudaStream_t stream);
+
+}  // namespace fathom

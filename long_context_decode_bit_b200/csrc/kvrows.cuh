@@ -31,7 +31,8 @@ constexpr int kRowsThreads = 32 * kRowsWarps;
 
 // Query row tiles of a call and their split over the tokens.
 struct KvSplit {
-    int32_t nt;          // 8-row tiles per CTA
+    int32_t nt;          // 8-row tiles per CTA, or 0: kvchunk.cuh takes the call
+    int32_t tile_rows;   // query rows per CTA
     int32_t row_tiles;   // CTAs along a sequence's query rows
     int32_t splits;      // CTAs along its tokens, at most
     int32_t chunk;       // tokens of a stretch
@@ -62,10 +63,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return r;
 }
 
+// 2^x to 2 ulp; below 2^-126 it is 0.
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float r;
-    asm("ex2.approx.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -490,7 +492,7 @@ kv_rows_kernel(const KvRowsArgs g)
             float top = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w * NT * 8 + nt * 8 + 2 * c + i]);
-            w8[nt][i] = top == -INFINITY ? 0.0f : exp2_fast(m[nt][i] - top);
+            w8[nt][i] = exp2_fast(m[nt][i] - (top == -INFINITY ? 0.0f : top));
         }
     for (int w = 0; w < kRowsWarps; ++w) {
         if (warp == w) {
@@ -515,9 +517,9 @@ kv_rows_kernel(const KvRowsArgs g)
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w * NT * 8 + row]);
-        if (top != -INFINITY)
+        const float low = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-            for (int w = 0; w < kRowsWarps; ++w) sum += sm_l[w * NT * 8 + row] * exp2_fast(sm_m[w * NT * 8 + row] - top);
+        for (int w = 0; w < kRowsWarps; ++w) sum += sm_l[w * NT * 8 + row] * exp2_fast(sm_m[w * NT * 8 + row] - low);
         // channel d = 8 VPB q + VPB r + j is kept at (VPB q + j) 8 + r
         const float x = os[row * (D + 8) + ((d / (8 * S::VPB)) * S::VPB + d % S::VPB) * 8 + (d / S::VPB) % 8];
         const int64_t head = ((sp.first + qr / G) * a.c.H + h) * G + qr % G;
@@ -529,7 +531,7 @@ kv_rows_kernel(const KvRowsArgs g)
                 g.pl[at_p] = sum;
             }
         } else {
-            const float y = top == -INFINITY ? 0.0f : x / sum;
+            const float y = sum == 0.0f ? 0.0f : x / sum;   // no token was seen (NaN scores make the sum NaN)
             if (QT == FATHOM_KEYS_F32) static_cast<float*>(a.out)[head * D + d] = y;
             else static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16(y);
         }

@@ -1,0 +1,117 @@
+"""Attention of prompt chunks over the paged cache against the 64-bit oracle, at the places where its tiles (256 query
+rows, 128 tokens), its ring of tiles and its stretches of tokens begin and end."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv as okv
+from _kv import TYPES, check_attention, fill, host, make_batch, make_cache
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def queries(shape, seed, dtype=torch.bfloat16, loud=2.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (loud * torch.randn(shape, generator=g, device=DEV)).to(dtype)
+
+
+def both(fathom, cache, fmt, q, table, cu, length, new, most, causal=True, scale=None):
+    out = fathom.paged_attention(cache, q, table, cu, length, new, most, causal=causal, scale=scale)
+    ref = okv.attend(host(cache), fmt, q.float().cpu().numpy(), table.cpu().numpy(), cu.cpu().numpy(), length.cpu().numpy(),
+                     cache.D ** -0.5 if scale is None else scale, causal)
+    check_attention(out, ref, most, cache.D, q.dtype)
+    return out
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("H,G,D,page,lens", [
+    (1, 1, 128, 64, [(128, 128)]),                    # one row tile, one tile of tokens
+    (1, 1, 128, 64, [(129, 129), (127, 127)]),
+    (1, 8, 64, 16, [(32, 128), (33, 129), (31, 1)]),  # one row over a row tile
+    (1, 2, 128, 16, [(128, 256), (128, 255), (128, 257)]),
+    (2, 4, 128, 128, [(65, 2000)]),                   # the ring goes round
+    (1, 3, 64, 32, [(200, 3001)]),
+    (1, 5, 128, 256, [(260, 1500), (1, 900), (0, 10)]),
+    (3, 7, 64, 64, [(19, 700), (100, 101)]),
+])
+def test_edges_of_tiles(fathom_gpu, fmt, causal, H, G, D, page, lens):
+    lens = [(min(n, t), t) for n, t in lens]
+    pages, table, cu, length = make_batch(lens, page, seed=D + G)
+    cache = make_cache(fathom_gpu, fmt, pages, H, D, page, ("head", "token", "layer")[(G + H) % 3])
+    fill(fathom_gpu, cache, lens, table, seed=G)
+    q = queries((int(cu[-1]), H * G, D), 4)
+    both(fathom_gpu, cache, fmt, q, table, cu, length, max(n for n, _ in lens), max(t for _, t in lens), causal)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_maximum_that_keeps_growing(fathom_gpu, fmt, D):
+    """Keys that point at the queries more and more along the sequence, by steps smaller and larger than the 2^8 below
+    which the running maximum stays; then the other way round."""
+    lens = [(150, 1300)]
+    pages, table, cu, length = make_batch(lens, 64)
+    base = torch.randn(D, generator=torch.Generator().manual_seed(1)).to(DEV)
+    for grow in (0.002, 0.02, 0.2, -0.02):
+        cache = make_cache(fathom_gpu, fmt, pages, 1, D, 64)
+        t = torch.arange(1300, device=DEV, dtype=torch.float32)
+        k = (base[None] * (grow * (t if grow > 0 else t - 1300))[:, None] + 0.1 * queries((1300, D), 5, torch.float32))[:, None]
+        v = queries((1300, 1, D), 6, torch.float32)
+        one = torch.tensor([0, 1300], dtype=torch.int32, device=DEV)
+        fathom_gpu.kv_write(cache, k.contiguous(), v, table, one, length)
+        q = (base[None, None] + 0.1 * queries((150, 2, D), 7, torch.float32)).to(torch.bfloat16)
+        both(fathom_gpu, cache, fmt, q, table, cu, length, 150, 1300)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("new", [1, 100])
+def test_pages_missing_in_the_middle(fathom_gpu, new, dtype):
+    """Entries of the table that name no page: their tokens are left out, by whole tiles and within tiles."""
+    for page in (16, 64, 256):
+        lens = [(new, 1500), (new, 700)]
+        pages, table, cu, length = make_batch(lens, page)
+        cache = make_cache(fathom_gpu, "int8", pages, 2, 128, page)
+        fill(fathom_gpu, cache, lens, table)
+        table[0, 1] = -1
+        table[0, 3:3 + 256 // page] = pages
+        table[1, 0] = 1 << 30
+        table[1, 2] = -7
+        both(fathom_gpu, cache, "int8", queries((2 * new, 8, 128), 4, TYPES[dtype]), table, cu, length, new, 1500)
+
+
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "e4m3"])
+def test_nan_keys_are_not_hidden(fathom_gpu, fmt, new):
+    """A NaN among the keys a row sees makes the row NaN, also where no other key is left; other sequences stay."""
+    lens = [(new, new), (new, new + 30)]
+    pages, table, cu, length = make_batch(lens, 64)
+    cache = make_cache(fathom_gpu, fmt, pages, 1, 128, 64)
+    k, v = torch.ones(2 * new + 30, 1, 128, device=DEV), torch.ones(2 * new + 30, 1, 128, device=DEV)
+    k[:new] = float("nan")
+    everything = torch.tensor([0, new, 2 * new + 30], dtype=torch.int32, device=DEV)
+    fathom_gpu.kv_write(cache, k, v, table, everything, length)
+    for dt in TYPES.values():
+        out = fathom_gpu.paged_attention(cache, queries((2 * new, 4, 128), 4, dt), table, cu, length, new, new + 30)
+        assert out[:new].isnan().all() and not out[new:].isnan().any()
+
+
+def test_many_stretches(fathom_gpu):
+    """A session long enough for the tokens to be cut into stretches, against the same call cut otherwise (bounded by a
+    larger max_len) within the bound of both, and run twice with equal results."""
+    n = 20000
+    for new, G in ((1, 4), (12, 2), (40, 4), (300, 2)):
+        lens = [(new, n)]
+        pages, table, cu, length = make_batch(lens, 64)
+        cache = make_cache(fathom_gpu, "int8", pages, 1, 128, 64)
+        fill(fathom_gpu, cache, lens, table)
+        q = queries((new, G, 128), 4)
+        few = torch.arange(0, new, 1 + new // 8)
+        ref = okv.attend(host(cache), "int8", q.float().cpu().numpy(), table.cpu().numpy(), cu.cpu().numpy(),
+                         length.cpu().numpy(), 128 ** -0.5)
+        ref = tuple(np.asarray(x)[few.numpy()] for x in ref)
+        out = fathom_gpu.paged_attention(cache, q, table, cu, length, new, n)
+        assert torch.equal(out, fathom_gpu.paged_attention(cache, q, table, cu, length, new, n))
+        check_attention(out[few], ref, n, 128, torch.bfloat16)
+        check_attention(fathom_gpu.paged_attention(cache, q, table, cu, length, new, 100 * n)[few], ref, n, 128, torch.bfloat16)
+    assert fathom_gpu.device_status() == fathom_gpu.OK
