@@ -174,11 +174,6 @@ __device__ __forceinline__ void st_shared16(uint32_t at, uint4 x)
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
 
-__device__ __forceinline__ void cp_async16_to(uint32_t at, const void* gmem, int bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(at), "l"(gmem), "r"(bytes) : "memory");
-}
-
 // Page of the 16 tokens from `at` + 16*lane (lanes 0..7), -1 for none of this stretch's.
 __device__ __forceinline__ int chunk_page(const KvCache& c, const int32_t* table, int table_pages, int at, int end, int lane)
 {
@@ -234,6 +229,7 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
     } else {
         constexpr int PIECES = D / 16, ROWS = 128 / PIECES, N = 128 / ROWS;   // 16 codes to a piece
         const int piece = t % PIECES, r0 = t / PIECES;
+        const CodeMasks masks = code_masks<FMT>();
         uint4 raw[N];
         uint32_t pw[N];
         auto fetch = [&](int at, bool v) {
@@ -270,9 +266,9 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
                     uint4 o[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        o[k] = make_uint4(decode2<FMT, 0, 1>(w[2 * k], w[2 * k], f), decode2<FMT, 2, 3>(w[2 * k], w[2 * k], f),
-                                          decode2<FMT, 0, 1>(w[2 * k + 1], w[2 * k + 1], f),
-                                          decode2<FMT, 2, 3>(w[2 * k + 1], w[2 * k + 1], f));
+                        o[k] = make_uint4(decode2<FMT, 0, 1>(w[2 * k], w[2 * k], f, masks), decode2<FMT, 2, 3>(w[2 * k], w[2 * k], f, masks),
+                                          decode2<FMT, 0, 1>(w[2 * k + 1], w[2 * k + 1], f, masks),
+                                          decode2<FMT, 2, 3>(w[2 * k + 1], w[2 * k + 1], f, masks));
                     // half of the threads store their second piece first: 8 threads then fill all banks once
                     const int first = (piece >> 2) & 1;
                     const uint32_t to = ring + st * S::TILE;

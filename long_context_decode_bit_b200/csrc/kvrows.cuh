@@ -1,28 +1,32 @@
 // Attention of few query rows over rows of the paged cache, on the matrix
-// units a warp drives by itself (mma.sync, m16n8k16, bf16): single tokens,
-// the union of the scan's winners, and what kvchunk.cu does not take (fp32
+// units a warp drives by itself (mma.sync, m16n8k16): single tokens, the
+// union of the scan's winners, and what kvchunk.cuh does not take (fp32
 // queries, widths other than 64 and 128).
 //
 // The work is bound by reading K and V, so the products are turned round to
 // have the cached rows as the 16-row operand and the (few) query rows as the
-// 8-column one, and no cached byte passes through shared memory:
+// 8-column one:
 //   S^T [16 keys x 8 rows] = K [16 x D] Q^T,  O^T [D x 8] += V^T [D x 16] P^T.
-// A dot product may run over the channels in any order, so a lane's operand
-// registers for K are simply consecutive bytes of one row (16-byte loads,
-// whole sectors), and Q is laid out in shared memory to match.  For V a lane
-// holds the same channels of the keys 2c, 2c+1, 2c+8, 2c+9 and pairs the keys
-// with byte permutes.  P^T comes out of S^T's registers by transposing 8x8
-// tiles in registers (movmatrix).  8-bit codes become bf16 in a lane's
-// registers, exactly: INT8 as 128 + low bits minus 128 or 256, E4M3 by moving
-// its fields, then times the block's power of two.
+// P^T comes out of S^T's registers by transposing 8x8 tiles in registers
+// (movmatrix).  A CTA takes 8*NT query rows of one sequence and group and one
+// stretch of its tokens; its four warps take 16-key tiles in turn.  Each has
+// a ring of its own for them, filled by cp.async (zeros for keys that are not
+// there), so that no warp waits for another until the end, where maxima and
+// sums are joined in shared memory.  Stretches are joined by kv_join_kernel
+// in a fixed order, so results do not depend on timing.
 //
-// A CTA takes 8*NT query rows of one sequence and group and one stretch of
-// its tokens; its four warps take 16-key tiles in turn, each with its own
-// running maximum and sums, joined in shared memory.  Stretches are joined
-// by kv_join_kernel in a fixed order, so results do not depend on timing.
+// 16-bit rows are operands as they are (ldmatrix, V transposed).  8-bit codes
+// become bf16 on their way to the operand registers, exactly: INT8 as
+// 128 + low bits less 128 or 256, E4M3 by moving its fields, times the block's
+// power of two.  (fp16 operands take two instructions less to a pair of INT8
+// codes, but then powers have to be kept relative to a running largest and
+// weights below 2^-40 are lost; both took the same time.)  A dot product may
+// run over the channels in any order, so a lane takes consecutive bytes of a
+// row, and Q is laid out to match.
 #pragma once
 
 #include "kv.cuh"
+#include "ring.cuh"
 
 namespace fathom {
 
@@ -71,19 +75,6 @@ __device__ __forceinline__ float exp2_fast(float x)
     return r;
 }
 
-// NW words of a row, read once.
-template <int NW>
-__device__ __forceinline__ void load_words(const unsigned char* p, uint32_t* w)
-{
-    if (NW == 4)
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-    else if (NW == 2)
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-    else
-        asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];\n" : "=r"(w[0]) : "l"(p));
-}
-
 __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b)
 {
     uint32_t r;
@@ -98,20 +89,49 @@ __device__ __forceinline__ uint32_t bsub2(uint32_t a, uint32_t b)
     return r;
 }
 
-// Bytes BLO of x and BHI of y as bf16 values times the powers `f` (bf16x2).
-template <int FMT, int BLO, int BHI>
-__device__ __forceinline__ uint32_t decode2(uint32_t x, uint32_t y, uint32_t f)
+// (x & y) | z
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t y, uint32_t z)
 {
-    if (FMT == FATHOM_KV_INT8) {
-        // the byte in the low half of each 16 bits (the byte above it is cut off)
-        const uint32_t t = __byte_perm(x, y, BLO | (BLO << 4) | ((4 + BHI) << 8) | ((4 + BHI) << 12));
-        const uint32_t low = (t & 0x007f007fu) | 0x43004300u;    // 128 + low 7 bits
-        const uint32_t off = (t & 0x00800080u) | 0x43004300u;    // 128, or 256 for a negative code
-        return bmul2(bsub2(low, off), f);
-    }
-    // the byte on top: sign in place, exponent and mantissa 4 below; 2^120 of the power makes up for the bias
-    const uint32_t t = __byte_perm(x, y, (BLO << 4) | BLO | ((4 + BHI) << 12) | ((4 + BHI) << 8));
-    return bmul2(((t >> 4) & 0x07f007f0u) | (t & 0x80008000u), f);
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+    return r;
+}
+
+// Masks of the decoders, kept in registers: an instruction takes one constant only.
+struct CodeMasks {
+    uint32_t a, b, c;
+};
+
+template <int FMT>
+__device__ __forceinline__ CodeMasks code_masks()
+{
+    CodeMasks m;
+    asm volatile("mov.b32 %0, %3;\n mov.b32 %1, %4;\n mov.b32 %2, %5;\n"
+                 : "=r"(m.a), "=r"(m.b), "=r"(m.c)
+                 : "n"(FMT == FATHOM_KV_INT8 ? 0x007f007f : 0x07f007f0), "n"(FMT == FATHOM_KV_INT8 ? 0x00800080 : 0x80008000),
+                   "n"(0x43004300));
+    return m;
+}
+
+// INT8 codes in the low bytes of each 16 bits as bf16 values, times the powers f:
+// 128 + low 7 bits, less 128, or 256 for a negative code.
+__device__ __forceinline__ uint32_t decode_low(uint32_t t, uint32_t f, const CodeMasks& m)
+{
+    return bmul2(bsub2(and_or(t, m.a, m.c), and_or(t, m.b, m.c)), f);
+}
+
+// E4M3 codes in the high bytes: sign in place, exponent and mantissa 4 below; 2^120 of the power makes up for the bias.
+__device__ __forceinline__ uint32_t decode_high(uint32_t t, uint32_t f, const CodeMasks& m)
+{
+    return bmul2(and_or(t, m.b, (t >> 4) & m.a), f);
+}
+
+// Bytes BLO of x and BHI of y.
+template <int FMT, int BLO, int BHI>
+__device__ __forceinline__ uint32_t decode2(uint32_t x, uint32_t y, uint32_t f, const CodeMasks& m)
+{
+    if (FMT == FATHOM_KV_INT8) return decode_low(__byte_perm(x, y, BLO | ((4 + BHI) << 8)), f, m);
+    return decode_high(__byte_perm(x, y, (BLO << 4) | ((4 + BHI) << 12)), f, m);
 }
 
 // The 16 bits that decode2 multiplies with, from the exponent byte.
@@ -119,6 +139,19 @@ template <int FMT>
 __device__ __forceinline__ uint32_t pow_bits(uint32_t byte)
 {
     return (FMT == FATHOM_KV_INT8 ? byte : min(byte + 120u, 255u)) << 7;
+}
+
+// Operands of the 4 codes of a word, codes (0, 2) and (1, 3), times the powers f.
+template <int FMT>
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t f, const CodeMasks& m, uint32_t* a, uint32_t* b)
+{
+    if (FMT == FATHOM_KV_INT8) {
+        *a = decode_low(w, f, m);
+        *b = decode_low(w >> 8, f, m);
+    } else {
+        *a = decode_high(w << 8, f, m);
+        *b = decode_high(w, f, m);
+    }
 }
 
 // x as bf16 parts that sum to it (to 8 bits each).
@@ -160,32 +193,102 @@ __device__ __forceinline__ int kv_tile_keys(const KvAttend& a, const KvSpan& s, 
     return max(0, min(s.keys, s.pos0 + last / a.G + 1));
 }
 
-template <int D, int FMT, int QT, int NT, bool UNION>
+// NW words from shared memory.
+template <int NW>
+__device__ __forceinline__ void lds_words(uint32_t at, uint32_t* w)
+{
+    if (NW == 4)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+    else if (NW == 2)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+    else
+        asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(w[0]) : "r"(at));
+}
+
+__device__ __forceinline__ int lds_byte(uint32_t at)
+{
+    uint32_t r;
+    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(r) : "r"(at));
+    return static_cast<int>(r);
+}
+
+// Four 8x8 tiles of 16-bit values, rows at the lanes' addresses.
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d)
+{
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                     : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(at));
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                     : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(at));
+}
+
+// 16-byte copy to shared memory.
+__device__ __forceinline__ void cp_async16_to(uint32_t at, const void* gmem)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(at), "l"(gmem) : "memory");
+}
+
+// The same, of zeros where `bytes` is 0.
+__device__ __forceinline__ void cp_async16_to(uint32_t at, const void* gmem, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(at), "l"(gmem), "r"(bytes) : "memory");
+}
+
+template <int D, int FMT, int QT, int NT>
 struct RowsShape {
-    static constexpr int NQ = QT == FATHOM_KEYS_F32 ? 3 : 1;                   // bf16 parts of a query
-    static constexpr int NP = QT == FATHOM_KEYS_F32 ? 3 : (NT == 1 ? 2 : 1);   // and of a weight
+    static constexpr bool CODED = FMT != FATHOM_KV_BF16;
+    static constexpr bool WIDEQ = QT == FATHOM_KEYS_F32;
+    static constexpr int NQ = WIDEQ ? 3 : 1, NP = NQ;                              // parts of a query and of a weight
     static constexpr int ESZ = kv_elem_bytes<FMT>();
-    static constexpr int KPB = FMT == FATHOM_KV_BF16 ? 8 : (D % 64 == 0 ? 16 : 8);                        // channels of a K piece
-    static constexpr int VPB = FMT == FATHOM_KV_BF16 ? (D % 64 == 0 ? 8 : 4)
-                                                     : (D % 128 == 0 ? 16 : (D % 64 == 0 ? 8 : 4));       // and of a V piece
-    static constexpr int KPW = KPB * ESZ / 4, VPW = VPB * ESZ / 4;   // words of a piece
-    static constexpr int KP = D / (4 * KPB), VP = D / (8 * VPB);     // pieces of a lane's row
-    static constexpr int KS = D / 16;                                // matrix steps
-    static constexpr size_t QB = sizeof(uint2) * NQ * KS * NT * 32;   // bytes of Q's operand registers
-    static constexpr size_t OB = sizeof(float) * NT * 8 * (D + 8);    // and of the value sums
-    static constexpr size_t SUMS = QB > OB ? QB : OB;
-    static constexpr size_t SMEM = SUMS + sizeof(float) * 2 * kRowsWarps * NT * 8;
+    static constexpr int RB = D * ESZ, PP = RB / 16;                               // bytes of a row, and 16-byte pieces
+    static constexpr int KPB = D % 64 == 0 ? 16 : 8;                               // codes that a lane takes of a K row at a time
+    static constexpr int VPB = D % 128 == 0 ? 16 : (D % 64 == 0 ? 8 : 4);          // and of a V row
+    static constexpr int KPW = KPB / 4, VPW = VPB / 4;
+    static constexpr int KP = D / (4 * KPB), VP = D / (8 * VPB);
+    static constexpr int KS = D / 16;                                              // matrix steps
+    static constexpr int NB = D / kKvBlock, SBW = NB <= 4 ? 4 : 8;                 // exponent bytes of a row, and their place
+    static constexpr int LPR = PP % 4 == 0 ? 4 : 2, RPL = LPR / 2;                 // lanes that copy a row, rows of a lane
+    static constexpr int STAGE = 32 * RB + (CODED ? 32 * SBW : 0);                 // 16 rows of K and of V
+    static constexpr int STAGES = STAGE <= 2304 ? 5 : 3;
+    static constexpr int RING = kRowsWarps * STAGES * STAGE;
+    static constexpr int QB = static_cast<int>(sizeof(uint2)) * NQ * KS * NT * 32; // Q's operand registers
+    static constexpr int OB = static_cast<int>(sizeof(float)) * NT * 8 * (D + 8);  // value sums, where the ring was
+    static constexpr int SUMS = QB + (RING > OB ? RING : OB);
+    static constexpr int SMEM = SUMS + static_cast<int>(sizeof(float)) * NT * 8 * 2 * kRowsWarps;
+    static constexpr int FIT = 225 * 1024 / (SMEM + 1024);
+    static constexpr int CTAS = NT == 1 && D <= 128 ? (FIT < 4 ? FIT : 4) : (FIT < 2 ? FIT : 2);   // to an SM
+
+    // 16-byte piece of a row in its tile: moved so that the lanes that read together find different banks.
+    static __device__ __forceinline__ int swizzle(bool v, int row, int piece)
+    {
+        if (!CODED) return PP % 8 == 0 ? piece ^ (row & 7) : piece ^ ((row >> 1) & 3);
+        if (PP % 8 != 0) return piece;
+        return v ? piece ^ (((row >> 1) & 3) << 1) : piece ^ ((row & 1) << 2);
+    }
+    static __device__ __forceinline__ uint32_t at(bool v, int row, int piece)
+    {
+        return (v ? 16 * RB : 0) + row * RB + swizzle(v, row, piece) * 16;
+    }
+    // From the address of a row's piece p below N to that of piece p + N*i (N a power of two, tiles on 128 bytes).
+    template <int N>
+    static __device__ __forceinline__ uint32_t step(uint32_t from, int i)
+    {
+        const int span = PP % 8 == 0 ? 8 : (CODED ? 1 : 4);   // pieces among which a row's are moved
+        return N >= span ? from + 16 * N * i : (from ^ (16 * N * (i % (span / N)))) + 16 * span * (i / (span / N));
+    }
 };
 
 template <int D, int FMT, int QT, int NT, bool UNION>
-__global__ void __launch_bounds__(kRowsThreads, NT == 1 && D <= 128 ? 4 : 2)
+__global__ void __launch_bounds__(kRowsThreads, RowsShape<D, FMT, QT, NT>::CTAS)
 kv_rows_kernel(const KvRowsArgs g)
 {
-    using S = RowsShape<D, FMT, QT, NT, UNION>;
-    constexpr bool CODED = FMT != FATHOM_KV_BF16;
-    extern __shared__ __align__(16) unsigned char smem[];
-    uint2* qf = reinterpret_cast<uint2*>(smem);              // [NQ][KS][NT][32] operand registers of Q^T
-    float* os = reinterpret_cast<float*>(smem);              // [NT*8][D+8] value sums, after the loop
+    using S = RowsShape<D, FMT, QT, NT>;
+    constexpr bool CODED = S::CODED;
+    extern __shared__ __align__(128) unsigned char smem[];
+    uint2* qf = reinterpret_cast<uint2*>(smem);                       // [NQ][KS][NT][32] operand registers of Q^T
+    float* os = reinterpret_cast<float*>(smem + S::QB);               // [NT*8][D+8] value sums, after the loop
     float* sm_m = reinterpret_cast<float*>(smem + S::SUMS);
     float* sm_l = sm_m + kRowsWarps * NT * 8;
 
@@ -212,28 +315,140 @@ kv_rows_kernel(const KvRowsArgs g)
     const int end = min(keys, begin + g.s.chunk);
     if (begin >= keys && split > 0) return;   // the join knows
 
-    // Q^T operand registers: lane (r, c) of step ks holds channels of row r that match K's.
-    for (int e = threadIdx.x; e < S::KS * NT * 32; e += kRowsThreads) {
-        const int el = e & 31, nt = (e >> 5) % NT, ks = (e >> 5) / NT;
-        const int qr = r0 + nt * 8 + (el >> 2);
-        const int d = (ks / (S::KPB / 4)) * 4 * S::KPB + (el & 3) * S::KPB + (ks % (S::KPB / 4)) * 4;
-        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (qr < sp.rows * G) {
-            const int64_t at = (sp.first + qr / G) * a.q_tok + (static_cast<int64_t>(h) * G + qr % G) * a.q_head + d;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[j] = QT == FATHOM_KEYS_F32 ? static_cast<const float*>(a.q)[at + j]
-                                             : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at + j]);
+    // ---- bringing tiles.  A lane copies piece lane % LPR, + LPR, ... of the rows lane / LPR (and + 8).
+    const uint32_t ring = smem_addr(smem) + S::QB + warp * (S::STAGES * S::STAGE);
+    const int lr = lane / S::LPR, lq = lane % S::LPR;
+    const unsigned char* k_lane = a.c.k + h * a.c.head_stride + (UNION ? 0 : lr * a.c.token_stride) + lq * 16;
+    const unsigned char* v_lane = a.c.v + h * a.c.head_stride + (UNION ? 0 : lr * a.c.token_stride) + lq * 16;
+    // and the exponent bytes of row lane % 16 of K (lanes below 16) or V
+    const unsigned char* s_lane =
+        CODED ? (lane < 16 ? a.c.ks : a.c.vs) + h * a.c.shead_stride + (UNION ? 0 : (lane & 15) * a.c.stoken_stride) : nullptr;
+    int pos1 = -1, pos2 = -1, page1 = -1;      // the next tile's page (union: key lane's, and the one's after it)
+    int live_of[S::STAGES];                    // which keys of a held tile there are (kept in step with the ring)
+    uint32_t sc[2] = {0, 0};                   // exponent bytes on their way
+    int to_issue = begin + 16 * warp, slot = 0;
+    const uint32_t k_to = S::at(false, lr, lq), v_to = S::at(true, lr, lq);
+
+    auto union_at = [&](int at) { return lane < 16 && at + lane < end ? __ldg(a.uni + h * a.M + at + lane) : -1; };
+    auto place = [&](int pos) {
+        return pos >= 0 && (!UNION || pos < a.n) ? kv_page(a.c, table, a.w.table_pages, pos) : -1;
+    };
+    auto issue = [&]() {   // the tile at to_issue, into `slot`; the exponents of the one before to theirs
+        if (CODED) {
+            const uint32_t at = ring + (slot == 0 ? S::STAGES - 1 : slot - 1) * S::STAGE + 32 * S::RB + lane * S::SBW;
+            if (S::SBW == 4) asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(at), "r"(sc[0]) : "memory");
+            else asm volatile("st.shared.v2.u32 [%0], {%1,%2};\n" ::"r"(at), "r"(sc[0]), "r"(sc[1]) : "memory");
         }
+        const int at = to_issue;
+        to_issue = min(at, end) + 16 * kRowsWarps;
+        int live = 0;
+        if (at < end) {
+            const uint32_t dst = ring + slot * S::STAGE;
+            const unsigned char *kp[S::RPL], *vp[S::RPL], *sp_;
+            if (UNION) {
+                const int tok = pos1 & (a.c.page_tokens - 1);
+                live = static_cast<int>(__ballot_sync(0xffffffffu, page1 >= 0) & 0xffffu);
+                const int64_t off = page1 >= 0 ? page1 * a.c.page_stride + tok * a.c.token_stride : 0;
+                const int64_t soff = CODED && page1 >= 0 ? page1 * a.c.spage_stride + tok * a.c.stoken_stride : 0;
+#pragma unroll
+                for (int j = 0; j < S::RPL; ++j) {
+                    const int64_t o = __shfl_sync(0xffffffffu, off, lr + 8 * j);
+                    kp[j] = k_lane + o;
+                    vp[j] = v_lane + o;
+                }
+                sp_ = s_lane + __shfl_sync(0xffffffffu, soff, lane & 15);
+            } else {
+                const int tok = at & (a.c.page_tokens - 1);
+                live = page1 < 0 ? 0 : (end - at >= 16 ? 0xffff : (1 << (end - at)) - 1);
+                const int64_t off = page1 >= 0 ? page1 * a.c.page_stride + tok * a.c.token_stride : 0;
+#pragma unroll
+                for (int j = 0; j < S::RPL; ++j) {
+                    kp[j] = k_lane + off + 8 * j * a.c.token_stride;
+                    vp[j] = v_lane + off + 8 * j * a.c.token_stride;
+                }
+                sp_ = s_lane + (page1 >= 0 ? page1 * a.c.spage_stride + tok * a.c.stoken_stride : 0);
+            }
+            if (live == 0xffff) {
+#pragma unroll
+                for (int j = 0; j < S::RPL; ++j)
+#pragma unroll
+                    for (int i = 0; i < S::PP / S::LPR; ++i) {
+                        cp_async16_to(S::template step<S::LPR>(dst + k_to, i) + 8 * j * S::RB, kp[j] + 16 * S::LPR * i);
+                        cp_async16_to(S::template step<S::LPR>(dst + v_to, i) + 8 * j * S::RB, vp[j] + 16 * S::LPR * i);
+                    }
+            } else {
+#pragma unroll
+                for (int j = 0; j < S::RPL; ++j) {
+                    const bool on = (live >> (lr + 8 * j)) & 1;
+                    const unsigned char* kf = on ? kp[j] : a.c.k;   // dead rows' addresses are not used: their size is 0
+                    const unsigned char* vf = on ? vp[j] : a.c.v;
+#pragma unroll
+                    for (int i = 0; i < S::PP / S::LPR; ++i) {
+                        cp_async16_to(S::template step<S::LPR>(dst + k_to, i) + 8 * j * S::RB, kf + 16 * S::LPR * i, on ? 16 : 0);
+                        cp_async16_to(S::template step<S::LPR>(dst + v_to, i) + 8 * j * S::RB, vf + 16 * S::LPR * i, on ? 16 : 0);
+                    }
+                }
+            }
+            if (CODED) {
+                const bool on = (live >> (lane & 15)) & 1;
+                sc[0] = sc[1] = 0;
+                if (on) {
+                    if (S::NB == 4) {
+                        sc[0] = __ldg(reinterpret_cast<const uint32_t*>(sp_));
+                    } else if (S::NB == 8) {
+                        sc[0] = __ldg(reinterpret_cast<const uint32_t*>(sp_));
+                        sc[1] = __ldg(reinterpret_cast<const uint32_t*>(sp_) + 1);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < S::NB; ++i) sc[i >> 2] |= static_cast<uint32_t>(__ldg(sp_ + i)) << (8 * (i & 3));
+                    }
+                }
+            }
+            if (UNION) {
+                pos1 = pos2;
+                page1 = place(pos1);
+                pos2 = union_at(at + 32 * kRowsWarps);
+            } else {
+                page1 = at + 16 * kRowsWarps < end ? place(at + 16 * kRowsWarps) : -1;
+            }
+        }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+#pragma unroll
+        for (int i = 0; i + 1 < S::STAGES; ++i) live_of[i] = live_of[i + 1];
+        live_of[S::STAGES - 1] = live;
+        slot = slot + 1 == S::STAGES ? 0 : slot + 1;
+    };
+    if (UNION) {
+        pos1 = union_at(to_issue);
+        pos2 = union_at(to_issue + 16 * kRowsWarps);
+    } else {
+        pos1 = to_issue < end ? to_issue : -1;
+    }
+    page1 = place(pos1);
+#pragma unroll
+    for (int i = 0; i < S::STAGES; ++i) live_of[i] = 0;
+    for (int i = 0; i + 1 < S::STAGES; ++i) issue();
+
+    // ---- Q^T operand registers: lane (r, c) of step ks holds channels of row r that match K's.
+    auto query = [&](int qr, int d) {
+        if (qr >= sp.rows * G) return 0.0f;
+        const int64_t at = (sp.first + qr / G) * a.q_tok + (static_cast<int64_t>(h) * G + qr % G) * a.q_head + d;
+        return QT == FATHOM_KEYS_F32 ? static_cast<const float*>(a.q)[at]
+                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at]);
+    };
+    for (int e = threadIdx.x; e < S::KS * NT * 32; e += kRowsThreads) {
+        const int el = e & 31, nt = (e >> 5) % NT, ks = (e >> 5) / NT, qr = r0 + nt * 8 + (el >> 2);
         uint32_t lo[S::NQ], hi[S::NQ];
-        split2<S::NQ>(x[0], x[1], lo);
-        split2<S::NQ>(x[2], x[3], hi);
+        const int d = CODED ? (ks / S::KPW) * 4 * S::KPB + (el & 3) * S::KPB + (ks % S::KPW) * 4 : 16 * ks + 2 * (el & 3);
+        split2<S::NQ>(query(qr, d), query(qr, d + (CODED ? 2 : 1)), lo);
+        split2<S::NQ>(query(qr, d + (CODED ? 1 : 8)), query(qr, d + (CODED ? 3 : 9)), hi);
 #pragma unroll
         for (int p = 0; p < S::NQ; ++p) qf[((p * S::KS + ks) * NT + nt) * 32 + el] = make_uint2(lo[p], hi[p]);
     }
 
     // Last token that rows 2c, 2c+1 of each tile see (padding rows see all), and the least of any row.
     int seen[NT][2], least = 0x7fffffff;
+    const float log2s = a.scale * 1.4426950408889634f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -251,121 +466,28 @@ kv_rows_kernel(const KvRowsArgs g)
 #pragma unroll
         for (int t = 0; t < S::KS; ++t) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.0f;
     }
-    const float log2s = a.scale * 1.4426950408889634f;
     __syncthreads();
 
-    uint32_t kw[2][S::KP * S::KPW], vw[4][S::VP * S::VPW];
-    uint32_t kb[2][S::KP], vb[4][S::VP];   // exponent bytes of the pieces' blocks
-    int kpage, vpage = -1;
-    int live_k, live_v = 0, live_at;       // which of the tile's 16 keys there are
-    // A lane's keys: K rows r, r + 8; V rows 2c, 2c + 1, 2c + 8, 2c + 9.
-    // In a union each key has its own place, kept by lane (key) for the whole warp.
-    int upos = -1, upage = -1, vupos = 0, vupage = -1, unext = -1;
+    // Where a lane reads: rows r of K and 2c of V (the others lie 1 and 8 rows behind), or the rows ldmatrix asks for.
+    const uint32_t k_rd = CODED ? S::at(false, r, c * S::KPB >> 4) + (c * S::KPB & 15) : S::at(false, lane & 15, lane >> 4);
+    const uint32_t v_rd = CODED ? S::at(true, 2 * c, r * S::VPB >> 4) + (r * S::VPB & 15)
+                                : S::at(true, (lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1);
+    const uint32_t ks_rd = 32 * S::RB + r * S::SBW + (c * S::KPB >> 5);
+    const uint32_t vs_rd = 32 * S::RB + (16 + 2 * c) * S::SBW + (r * S::VPB >> 5);
+    const CodeMasks masks = code_masks<FMT>();
+    int cur = 0;
+    for (int at = begin + 16 * warp; at < end; at += 16 * kRowsWarps) {
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(S::STAGES - 2) : "memory");
+        __syncwarp();
+        const int live = live_of[1];   // the oldest tile but the one just used up
+        issue();
+        const uint32_t here = ring + cur * S::STAGE;
+        cur = cur + 1 == S::STAGES ? 0 : cur + 1;
 
-    auto find = [&](int at) {   // the places of the tile at `at`
-        live_at = at;
-        if (UNION) {
-            upos = unext;
-            upage = upos >= 0 && upos < a.n ? kv_page(a.c, table, a.w.table_pages, upos) : -1;
-            live_k = static_cast<int>(__ballot_sync(0xffffffffu, upage >= 0) & 0xffffu);
-            const int nx = at + 16 * kRowsWarps + lane;
-            unext = lane < 16 && nx < end ? __ldg(a.uni + h * a.M + nx) : -1;
-        } else {
-            kpage = at < end ? kv_page(a.c, table, a.w.table_pages, at) : -1;
-            const int n = end - at;
-            live_k = kpage < 0 ? 0 : (n >= 16 ? 0xffff : (1 << n) - 1);
-        }
-    };
-    auto load_k = [&]() {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int key = r + 8 * i;
-            int page = kpage, tok = (live_at + key) & (a.c.page_tokens - 1);
-            if (UNION) {
-                page = __shfl_sync(0xffffffffu, upage, key);
-                tok = __shfl_sync(0xffffffffu, upos, key) & (a.c.page_tokens - 1);
-            }
-            if ((live_k >> key) & 1) {
-                const unsigned char* p = a.c.k + kv_off(a.c, page, h, tok) + c * S::KPB * S::ESZ;
-#pragma unroll
-                for (int q = 0; q < S::KP; ++q) load_words<S::KPW>(p + q * 4 * S::KPB * S::ESZ, &kw[i][q * S::KPW]);
-                if (CODED) {
-                    const unsigned char* sc = a.c.ks + kv_scale_off(a.c, page, h, tok);
-                    if (D == 128) {
-                        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(sc));
-#pragma unroll
-                        for (int q = 0; q < S::KP; ++q) kb[i][q] = (w >> (8 * (2 * q + (c >> 1)))) & 0xff;
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < S::KP; ++q) kb[i][q] = __ldg(sc + ((q * 4 + c) * S::KPB >> 5));
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < S::KP * S::KPW; ++q) kw[i][q] = 0;
-#pragma unroll
-                for (int q = 0; q < S::KP; ++q) kb[i][q] = 0;
-            }
-        }
-    };
-    auto load_v = [&](int at) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = 2 * c + (i & 1) + 8 * (i >> 1);
-            int page = vpage, tok = (at + key) & (a.c.page_tokens - 1);
-            if (UNION) {
-                page = __shfl_sync(0xffffffffu, vupage, key);
-                tok = __shfl_sync(0xffffffffu, vupos, key) & (a.c.page_tokens - 1);
-            }
-            if ((live_v >> key) & 1) {
-                const unsigned char* p = a.c.v + kv_off(a.c, page, h, tok) + r * S::VPB * S::ESZ;
-#pragma unroll
-                for (int q = 0; q < S::VP; ++q) load_words<S::VPW>(p + q * 8 * S::VPB * S::ESZ, &vw[i][q * S::VPW]);
-                if (CODED) {
-                    const unsigned char* sc = a.c.vs + kv_scale_off(a.c, page, h, tok);
-#pragma unroll
-                    for (int q = 0; q < S::VP; ++q) vb[i][q] = __ldg(sc + ((q * 8 + r) * S::VPB >> 5));
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < S::VP * S::VPW; ++q) vw[i][q] = 0;
-#pragma unroll
-                for (int q = 0; q < S::VP; ++q) vb[i][q] = 0;
-            }
-        }
-    };
-
-    int at = begin + 16 * warp;
-    if (UNION) unext = lane < 16 && at + lane < end ? __ldg(a.uni + h * a.M + at + lane) : -1;
-    if (at < end) {
-        find(at);
-        load_k();
-    }
-    for (; at < end; at += 16 * kRowsWarps) {
-        vpage = kpage;
-        vupage = upage;
-        vupos = upos;
-        live_v = live_k;
-        load_v(at);
         float s[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < S::KS; ++ks) {
-            uint32_t a0, a1, a2, a3;
-            if (CODED) {
-                const int q = ks / (S::KPB / 4), w = q * S::KPW + ks % (S::KPB / 4);
-                const uint32_t f0 = pow_bits<FMT>(kb[0][q]) * 0x10001u, f1 = pow_bits<FMT>(kb[1][q]) * 0x10001u;
-                a0 = decode2<FMT, 0, 1>(kw[0][w], kw[0][w], f0);
-                a2 = decode2<FMT, 2, 3>(kw[0][w], kw[0][w], f0);
-                a1 = decode2<FMT, 0, 1>(kw[1][w], kw[1][w], f1);
-                a3 = decode2<FMT, 2, 3>(kw[1][w], kw[1][w], f1);
-            } else {
-                a0 = kw[0][2 * ks];
-                a2 = kw[0][2 * ks + 1];
-                a1 = kw[1][2 * ks];
-                a3 = kw[1][2 * ks + 1];
-            }
+        auto scores = [&](int ks, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
             for (int p = 0; p < S::NQ; ++p)
 #pragma unroll
@@ -373,17 +495,37 @@ kv_rows_kernel(const KvRowsArgs g)
                     const uint2 q = qf[((p * S::KS + ks) * NT + nt) * 32 + lane];
                     mma16816(s[nt], a0, a1, a2, a3, q.x, q.y);
                 }
-        }
-        // The next tile's keys are on their way while this one's weights are taken.
-        if (at + 16 * kRowsWarps < end) {
-            find(at + 16 * kRowsWarps);
-            load_k();
+        };
+        if constexpr (CODED) {
+#pragma unroll
+            for (int q = 0; q < S::KP; ++q) {
+                uint32_t w[2][S::KPW], f[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    lds_words<S::KPW>(S::template step<S::KPB / 4>(here + k_rd, q) + 8 * i * S::RB, w[i]);
+                    f[i] = pow_bits<FMT>(lds_byte(here + ks_rd + 8 * i * S::SBW + (q * 4 * S::KPB >> 5))) * 0x10001u;
+                }
+#pragma unroll
+                for (int j = 0; j < S::KPW; ++j) {
+                    uint32_t a0, a1, a2, a3;
+                    codes4<FMT>(w[0][j], f[0], masks, &a0, &a2);
+                    codes4<FMT>(w[1][j], f[1], masks, &a1, &a3);
+                    scores(q * S::KPW + j, a0, a1, a2, a3);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < S::KS; ++ks) {
+                uint32_t a0, a1, a2, a3;
+                ldmatrix4<false>(S::template step<2>(here + k_rd, ks), a0, a1, a2, a3);
+                scores(ks, a0, a1, a2, a3);
+            }
         }
 
-        const bool whole = live_v == 0xffff && at + 15 <= least;
+        const bool whole = live == 0xffff && at + 15 <= least;
+        bool grew = false;
         uint32_t pb[NT][S::NP][2];
         float f[NT][2];
-        bool grew = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -391,7 +533,7 @@ kv_rows_kernel(const KvRowsArgs g)
                 s[nt][i] *= log2s;
                 if (!whole) {
                     const int key = r + 8 * (i >> 1);
-                    if (!((live_v >> key) & 1) || at + key > seen[nt][i & 1]) s[nt][i] = -INFINITY;
+                    if (!((live >> key) & 1) || at + key > seen[nt][i & 1]) s[nt][i] = -INFINITY;
                 }
             }
 #pragma unroll
@@ -403,10 +545,10 @@ kv_rows_kernel(const KvRowsArgs g)
                 const float old = m[nt][i];
                 grew |= top > old;
                 m[nt][i] = fmaxf(old, top);
-                const float base = m[nt][i] == -INFINITY ? 0.0f : m[nt][i];
-                f[nt][i] = exp2_fast(old - base);
-                s[nt][i] = exp2_fast(s[nt][i] - base);
-                s[nt][i + 2] = exp2_fast(s[nt][i + 2] - base);
+                const float low = m[nt][i] == -INFINITY ? 0.0f : m[nt][i];
+                f[nt][i] = exp2_fast(old - low);
+                s[nt][i] = exp2_fast(s[nt][i] - low);
+                s[nt][i + 2] = exp2_fast(s[nt][i + 2] - low);
                 l[nt][i] = l[nt][i] * f[nt][i] + (s[nt][i] + s[nt][i + 2]);
             }
             uint32_t lo[S::NP], hi[S::NP];
@@ -429,47 +571,45 @@ kv_rows_kernel(const KvRowsArgs g)
                     o[t][nt][3] *= f[nt][1];
                 }
         }
+        auto values = [&](int t, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-        for (int q = 0; q < S::VP; ++q) {
-            uint32_t f01 = 0, f89 = 0;
-            if (CODED) {
-                f01 = pow_bits<FMT>(vb[0][q]) | pow_bits<FMT>(vb[1][q]) << 16;
-                f89 = pow_bits<FMT>(vb[2][q]) | pow_bits<FMT>(vb[3][q]) << 16;
-            }
+            for (int p = 0; p < S::NP; ++p)
 #pragma unroll
-            for (int j = 0; j < S::VPB / 2; ++j) {
-                uint32_t a0, a1, a2, a3;
-                if (CODED) {
-                    const int w = q * S::VPW + j / 2;
-                    if (j & 1) {
-                        a0 = decode2<FMT, 2, 2>(vw[0][w], vw[1][w], f01);
-                        a1 = decode2<FMT, 3, 3>(vw[0][w], vw[1][w], f01);
-                        a2 = decode2<FMT, 2, 2>(vw[2][w], vw[3][w], f89);
-                        a3 = decode2<FMT, 3, 3>(vw[2][w], vw[3][w], f89);
-                    } else {
-                        a0 = decode2<FMT, 0, 0>(vw[0][w], vw[1][w], f01);
-                        a1 = decode2<FMT, 1, 1>(vw[0][w], vw[1][w], f01);
-                        a2 = decode2<FMT, 0, 0>(vw[2][w], vw[3][w], f89);
-                        a3 = decode2<FMT, 1, 1>(vw[2][w], vw[3][w], f89);
-                    }
-                } else {
-                    const int w = q * S::VPW + j;
-                    a0 = __byte_perm(vw[0][w], vw[1][w], 0x5410);
-                    a1 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
-                    a2 = __byte_perm(vw[2][w], vw[3][w], 0x5410);
-                    a3 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+                for (int nt = 0; nt < NT; ++nt) mma16816(o[t][nt], a0, a1, a2, a3, pb[nt][p][0], pb[nt][p][1]);
+        };
+        if constexpr (CODED) {
+#pragma unroll
+            for (int q = 0; q < S::VP; ++q) {
+                uint32_t w[4][S::VPW], p2[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int on = (i & 1) + 8 * (i >> 1);
+                    lds_words<S::VPW>(here + v_rd + on * S::RB + q * 8 * S::VPB, w[i]);
+                    p2[i] = pow_bits<FMT>(lds_byte(here + vs_rd + on * S::SBW + (q * 8 * S::VPB >> 5)));
                 }
+                const uint32_t f01 = p2[0] | p2[1] << 16, f89 = p2[2] | p2[3] << 16;
 #pragma unroll
-                for (int p = 0; p < S::NP; ++p)
+                for (int j = 0; j < S::VPW; ++j) {
+                    const int t = (q * S::VPB) / 2 + 2 * j;
+                    values(t, decode2<FMT, 0, 0>(w[0][j], w[1][j], f01, masks), decode2<FMT, 1, 1>(w[0][j], w[1][j], f01, masks),
+                           decode2<FMT, 0, 0>(w[2][j], w[3][j], f89, masks), decode2<FMT, 1, 1>(w[2][j], w[3][j], f89, masks));
+                    values(t + 1, decode2<FMT, 2, 2>(w[0][j], w[1][j], f01, masks), decode2<FMT, 3, 3>(w[0][j], w[1][j], f01, masks),
+                           decode2<FMT, 2, 2>(w[2][j], w[3][j], f89, masks), decode2<FMT, 3, 3>(w[2][j], w[3][j], f89, masks));
+                }
+            }
+        } else {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816(o[q * (S::VPB / 2) + j][nt], a0, a1, a2, a3, pb[nt][p][0], pb[nt][p][1]);
+            for (int t = 0; t < S::KS; ++t) {
+                uint32_t a0, a1, a2, a3;
+                ldmatrix4<true>(S::template step<2>(here + v_rd, t), a0, a1, a2, a3);
+                values(t, a0, a1, a2, a3);
             }
         }
     }
 
     // Join the warps.
-    __syncthreads();   // Q has been read
+    cp_async_wait_all();
+    __syncthreads();   // the rings have been read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -520,8 +660,9 @@ kv_rows_kernel(const KvRowsArgs g)
         const float low = top == -INFINITY ? 0.0f : top;
 #pragma unroll
         for (int w = 0; w < kRowsWarps; ++w) sum += sm_l[w * NT * 8 + row] * exp2_fast(sm_m[w * NT * 8 + row] - low);
-        // channel d = 8 VPB q + VPB r + j is kept at (VPB q + j) 8 + r
-        const float x = os[row * (D + 8) + ((d / (8 * S::VPB)) * S::VPB + d % S::VPB) * 8 + (d / S::VPB) % 8];
+        // with codes, channel d = 8 VPB q + VPB r + j is kept at (VPB q + j) 8 + r
+        const int kept = CODED ? ((d / (8 * S::VPB)) * S::VPB + d % S::VPB) * 8 + (d / S::VPB) % 8 : d;
+        const float x = os[row * (D + 8) + kept];
         const int64_t head = ((sp.first + qr / G) * a.c.H + h) * G + qr % G;
         if (parts) {
             const int64_t at_p = split * g.heads + head;
@@ -542,7 +683,7 @@ kv_rows_kernel(const KvRowsArgs g)
 template <int D, int FMT, int QT, int NT, bool UNION>
 int launch_rows_t(const KvRowsArgs& g, cudaStream_t stream)
 {
-    using S = RowsShape<D, FMT, QT, NT, UNION>;
+    using S = RowsShape<D, FMT, QT, NT>;
     const int st = ensure_dynamic_smem(reinterpret_cast<const void*>(kv_rows_kernel<D, FMT, QT, NT, UNION>), S::SMEM);
     if (st) return st;
     const dim3 grid(static_cast<unsigned>(g.s.splits) * g.s.row_tiles, static_cast<unsigned>(g.a.c.H),

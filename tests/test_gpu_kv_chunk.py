@@ -115,3 +115,25 @@ def test_many_stretches(fathom_gpu):
         check_attention(out[few], ref, n, 128, torch.bfloat16)
         check_attention(fathom_gpu.paged_attention(cache, q, table, cu, length, new, 100 * n)[few], ref, n, 128, torch.bfloat16)
     assert fathom_gpu.device_status() == fathom_gpu.OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("span", [10, 40])
+@pytest.mark.parametrize("D,new", [(128, 1), (96, 1), (64, 5), (128, 100), (256, 3)])
+def test_blocks_of_very_different_sizes(fathom_gpu, fmt, dtype, span, D, new):
+    """Powers of two 2^-span .. 2^span among the blocks of K, V and q, small blocks of K where q is large: operands hold
+    them all exactly."""
+    n = 300
+    lens = [(new, n)]
+    pages, table, cu, length = make_batch(lens, 64)
+    cache = make_cache(fathom_gpu, fmt, pages, 1, D, 64)
+    g = torch.Generator(device=DEV).manual_seed(span + D)
+    size = lambda *shape: torch.exp2(torch.randint(-span, span + 1, shape, generator=g, device=DEV).float())  # noqa: E731
+    chan = size(1, 1, D // 32, 1)
+    k = (queries((n, 1, D // 32, 32), 1, torch.float32) * chan).flatten(2)
+    v = (queries((n, 1, D // 32, 32), 2, torch.float32) * size(n, 1, D // 32, 1)).flatten(2)
+    cu_all = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    fathom_gpu.kv_write(cache, k.contiguous(), v.contiguous(), table, cu_all, length)
+    q = (queries((new, 4, D // 32, 32), 3, torch.float32) / chan).flatten(2).to(TYPES[dtype])
+    both(fathom_gpu, cache, fmt, q, table, cu, length, new, n)
