@@ -9,20 +9,20 @@ namespace fathom {
 namespace {
 
 constexpr int kSms = 148;        // the machine this library is written for; only the cut depends on it
-constexpr int kJoinThreads = 128;
-constexpr int kJoinWarps = kJoinThreads / 32;
 
 int64_t round_up(int64_t x, int64_t to) { return ceil_div(x, to) * to; }
 
 // Tiles of kChunkRows query rows, one CTA to an SM.  The cut into stretches
 // that ends soonest: waves of CTAs times a stretch's tiles of tokens (and
 // about three tiles' time to start and end a CTA).
-KvSplit chunk_split(int H, int B, int64_t qrows, int64_t max_len)
+KvSplit chunk_split(int H, int G, int64_t rows, int B, int64_t qrows, int64_t max_len)
 {
     KvSplit s{};
     s.tile_rows = kChunkRows;
     s.row_tiles = static_cast<int32_t>(ceil_div(qrows, kChunkRows));
-    const int64_t items = static_cast<int64_t>(B) * H * s.row_tiles, tiles = std::max<int64_t>(1, ceil_div(max_len, kChunkKeys));
+    // Sequences of a batch are uneven: no more row tiles than all its rows fill, and one begun by each sequence.
+    const int64_t items = H * std::min(static_cast<int64_t>(B) * s.row_tiles, ceil_div(rows * G, kChunkRows) + B - 1);
+    const int64_t tiles = std::max<int64_t>(1, ceil_div(max_len, kChunkKeys));
     int64_t best = 0, each = tiles;
     for (int64_t n = 1; n <= 32 && n <= tiles; ++n) {
         const int64_t len = ceil_div(tiles, n), cost = ceil_div(items * n, kSms) * (len + 3 + (n > 1 ? 1 : 0));
@@ -38,11 +38,11 @@ KvSplit chunk_split(int H, int B, int64_t qrows, int64_t max_len)
 
 // Tiles of 8*nt query rows by stretches of tokens.  A CTA's four warps want
 // 64 tokens at least each; four CTAs fit an SM.
-KvSplit rows_split(int H, int G, int D, int B, int64_t max_new, int64_t max_len, int q_dtype)
+KvSplit rows_split(int H, int G, int D, int64_t rows, int B, int64_t max_new, int64_t max_len, int q_dtype)
 {
     KvSplit s{};
     const int64_t qrows = max_new * G;
-    if (q_dtype == FATHOM_KEYS_BF16 && (D == 64 || D == 128) && qrows > 64) return chunk_split(H, B, qrows, max_len);
+    if (q_dtype == FATHOM_KEYS_BF16 && (D == 64 || D == 128) && qrows > 64) return chunk_split(H, G, rows, B, qrows, max_len);
     s.nt = qrows <= 8 ? 1 : (D <= 128 ? 4 : 2);
     s.tile_rows = 8 * s.nt;
     s.row_tiles = static_cast<int32_t>(ceil_div(qrows, s.tile_rows));
@@ -74,29 +74,32 @@ size_t parts_bytes(int64_t heads, int64_t splits, int D)
     return splits > 1 ? up256(sizeof(float) * splits * heads * D) + 2 * up256(sizeof(float) * splits * heads) : 0;
 }
 
-// One CTA per query head of a row: the stretches' value sums, each times
-// 2^(its maximum - the largest), over the weight sums treated alike.
-template <int QT>
-__global__ void __launch_bounds__(kJoinThreads)
+// The stretches' value sums, each times 2^(its maximum - the largest), over
+// the weight sums treated alike: WARPS warps to a query head of a row.  A
+// decode step's many stretches of few heads have 16, so that all loads are on
+// their way at once; a chunk's few stretches of many heads one, and 8 heads to
+// a CTA (a CTA each took 110 us for 65536 heads of 4 stretches).
+template <int QT, int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS)
 kv_join_kernel(const KvRowsArgs g)
 {
-    __shared__ float part[kJoinWarps][kMaxD];
-    __shared__ float part_l[kJoinWarps];
+    constexpr int HEADS = WARPS == 1 ? 8 : 1;   // of a CTA
     pdl_wait();
     const KvAttend& a = g.a;
-    const int D = a.c.D, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = blockIdx.x;
-    const int64_t head = row * gridDim.y + blockIdx.y;
+    const int D = a.c.D, lane = threadIdx.x & 31, heads_row = a.c.H * a.G;
+    const int warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
+    const int64_t head = static_cast<int64_t>(blockIdx.x) * HEADS + (WARPS == 1 ? threadIdx.x >> 5 : 0);
+    if (head >= g.heads) return;
+    const int row = static_cast<int>(head / heads_row), hq = static_cast<int>(head - static_cast<int64_t>(row) * heads_row);
     int n;   // stretches that were computed
     if (a.uni) {
-        const int h = blockIdx.y / a.G;
-        n = static_cast<int>(ceil_div(min(static_cast<int64_t>(max(a.count[h], 0)), a.M), g.s.chunk));
+        n = static_cast<int>(ceil_div(min(static_cast<int64_t>(max(a.count[hq / a.G], 0)), a.M), g.s.chunk));
     } else {
-        const int b = kv_sequence(a.w, static_cast<int>(row));
+        const int b = kv_sequence(a.w, row);
         if (b < 0) return;
         const KvSpan sp = kv_span(a, b);
-        const int qr = static_cast<int>(row - sp.first) * a.G + blockIdx.y % a.G;
         if (row - sp.first >= sp.rows) return;
+        const int qr = static_cast<int>(row - sp.first) * a.G + hq % a.G;
         const int r0 = qr / g.s.tile_rows * g.s.tile_rows;
         n = static_cast<int>(ceil_div(kv_tile_keys(a, sp, r0, g.s.tile_rows), g.s.chunk));
     }
@@ -109,7 +112,7 @@ kv_join_kernel(const KvRowsArgs g)
     for (int i = 0; i < kMaxD / 32; ++i) acc[i] = 0.0f;
     const float low = top == -INFINITY ? 0.0f : top;
 #pragma unroll 4
-    for (int s = warp; s < n; s += kJoinWarps) {
+    for (int s = warp; s < n; s += WARPS) {
         const int64_t at = s * g.heads + head;
         const float f = exp2_fast(g.pm[at] - low);
         l += g.pl[at] * f;
@@ -117,29 +120,45 @@ kv_join_kernel(const KvRowsArgs g)
         for (int i = 0; i < kMaxD / 32; ++i)
             if (i < D / 32) acc[i] = fmaf(g.po[at * D + lane + 32 * i], f, acc[i]);
     }
-#pragma unroll
-    for (int i = 0; i < kMaxD / 32; ++i)
-        if (i < D / 32) part[warp][lane + 32 * i] = acc[i];
-    if (lane == 0) part_l[warp] = l;
-    __syncthreads();
-    for (int d = threadIdx.x; d < D; d += kJoinThreads) {
-        float x = 0.0f, sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-            x += part[w][d];
-            sum += part_l[w];
-        }
+    auto store = [&](int d, float x, float sum) {
         const float y = sum == 0.0f ? 0.0f : x / sum;   // no token was seen (NaN scores make the sum NaN)
         if (QT == FATHOM_KEYS_F32) static_cast<float*>(a.out)[head * D + d] = y;
         else static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16(y);
+    };
+    if constexpr (WARPS == 1) {
+#pragma unroll
+        for (int i = 0; i < kMaxD / 32; ++i)
+            if (i < D / 32) store(lane + 32 * i, acc[i], l);
+    } else {
+        __shared__ float part[WARPS][kMaxD];
+        __shared__ float part_l[WARPS];
+#pragma unroll
+        for (int i = 0; i < kMaxD / 32; ++i)
+            if (i < D / 32) part[warp][lane + 32 * i] = acc[i];
+        if (lane == 0) part_l[warp] = l;
+        __syncthreads();
+        for (int d = threadIdx.x; d < D; d += 32 * WARPS) {
+            float x = 0.0f, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                x += part[w][d];
+                sum += part_l[w];
+            }
+            store(d, x, sum);
+        }
     }
+}
+
+template <int QT>
+int launch_join_t(const KvRowsArgs& g, cudaStream_t stream)
+{
+    if (g.s.splits > 16) return launch_pdl(kv_join_kernel<QT, 16>, static_cast<unsigned>(g.heads), 512, 0, stream, g);
+    return launch_pdl(kv_join_kernel<QT, 1>, static_cast<unsigned>(ceil_div(g.heads, 8)), 256, 0, stream, g);
 }
 
 int launch_join(const KvRowsArgs& g, int q_dtype, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>(g.a.uni ? 1 : g.a.w.rows), static_cast<unsigned>(g.a.c.H * g.a.G));
-    if (q_dtype == FATHOM_KEYS_F32) return launch_pdl(kv_join_kernel<FATHOM_KEYS_F32>, grid, kJoinThreads, 0, stream, g);
-    return launch_pdl(kv_join_kernel<FATHOM_KEYS_BF16>, grid, kJoinThreads, 0, stream, g);
+    return q_dtype == FATHOM_KEYS_F32 ? launch_join_t<FATHOM_KEYS_F32>(g, stream) : launch_join_t<FATHOM_KEYS_BF16>(g, stream);
 }
 
 }  // namespace
@@ -147,7 +166,7 @@ int launch_join(const KvRowsArgs& g, int q_dtype, cudaStream_t stream)
 size_t paged_attention_workspace_bytes(int H, int G, int D, int64_t rows, int B, int64_t max_new, int64_t max_len,
                                        int q_dtype)
 {
-    const KvSplit s = rows_split(H, G, D, B, std::min(max_new, rows), max_len, q_dtype);
+    const KvSplit s = rows_split(H, G, D, rows, B, std::min(max_new, rows), max_len, q_dtype);
     return parts_bytes(rows * H * G, s.splits, D);
 }
 
@@ -160,7 +179,7 @@ int launch_paged_attention(const KvAttend& a, int format, int q_dtype, void* ws,
 {
     KvRowsArgs g{};
     g.a = a;
-    g.s = a.uni ? union_split(a.c.H, a.M) : rows_split(a.c.H, a.G, a.c.D, a.w.B, a.max_new, a.max_len, q_dtype);
+    g.s = a.uni ? union_split(a.c.H, a.M) : rows_split(a.c.H, a.G, a.c.D, a.w.rows, a.w.B, a.max_new, a.max_len, q_dtype);
     g.heads = static_cast<int64_t>(a.w.rows) * a.c.H * a.G;
     unsigned char* base = static_cast<unsigned char*>(ws);
     if (g.s.splits > 1) {
@@ -173,6 +192,7 @@ int launch_paged_attention(const KvAttend& a, int format, int q_dtype, void* ws,
                    : format == FATHOM_KV_INT8 ? launch_rows_int8(g, q_dtype, stream)
                                               : launch_rows_e4m3(g, q_dtype, stream);
     if (st || g.s.splits <= 1) return st;
+    // heads < 2^31: there are stretches only where CTAs along rows and heads are few
     return launch_join(g, q_dtype, stream);
 }
 

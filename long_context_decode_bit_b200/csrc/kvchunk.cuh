@@ -146,19 +146,30 @@ __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.
 
 // ---- pairs of fp32
 
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float b)   // x = x a + b, y = y a + b
+__device__ __forceinline__ uint64_t pack2(float x, float y)
 {
-    asm("{\n .reg .b64 u, v, w;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %2};\n mov.b64 w, {%3, %3};\n fma.rn.f32x2 u, u, v, w;\n"
-        " mov.b64 {%0, %1}, u;\n}\n"
-        : "+f"(x), "+f"(y)
-        : "f"(a), "f"(b));
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+    return r;
 }
 
-__device__ __forceinline__ void add2(float& x, float& y, float a, float b)   // x += a, y += b
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y)
 {
-    asm("{\n .reg .b64 u, v;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %3};\n add.rn.f32x2 u, u, v;\n mov.b64 {%0, %1}, u;\n}\n"
-        : "+f"(x), "+f"(y)
-        : "f"(a), "f"(b));
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // ---- bringing K and V
@@ -181,6 +192,12 @@ __device__ __forceinline__ int chunk_page(const KvCache& c, const int32_t* table
     return lane < 8 && pos < end ? kv_page(c, table, table_pages, pos) : -1;
 }
 
+// Where those tokens are, from the start of K or V (-1: nowhere).
+__device__ __forceinline__ int64_t chunk_off(const KvCache& c, int page, int at, int h, int lane)
+{
+    return page < 0 ? -1 : kv_off(c, page, h, (at + 16 * lane) & (c.page_tokens - 1));
+}
+
 // The whole 128-token tiles of K and V from `begin` on, in the order K0 V0 K1 V1 ..., into the ring.
 template <int D, int FMT>
 __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* table, int table_pages, int h, int begin, int end,
@@ -195,9 +212,13 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
         constexpr int PIECES = D / 8, ROWS = 128 / PIECES;   // rows of a pass
         constexpr int AHEAD = S::STAGES - 2;                 // stages that may be on their way
         const int piece = t % PIECES, r0 = t / PIECES;
+        const uint32_t to0 = ring + tile_at(r0, piece);      // rows behind: the same place in the swizzle, ROWS being 8 or 16
+        const int64_t row_off = r0 * c.token_stride + piece * 16;
         int i = 0;
         for (int j = 0; j < tiles && ok; ++j) {
             const int at = begin + j * kChunkKeys;
+            const int64_t off = chunk_off(c, page, at, h, lane);
+            const bool whole = end - at >= kChunkKeys && __ballot_sync(0xffffffffu, page >= 0) == 0xff;
             next = chunk_page(c, table, table_pages, at + kChunkKeys, end, lane);
             for (int s = 0; s < 2; ++s, ++i) {
                 const int st = i % S::STAGES;
@@ -206,12 +227,15 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
                 const unsigned char* data = s ? c.v : c.k;
 #pragma unroll
                 for (int p = 0; p < 128 / ROWS; ++p) {
-                    const int row = r0 + p * ROWS;
-                    const int pg = __shfl_sync(0xffffffffu, page, row >> 4);
-                    const bool live = pg >= 0 && at + row < end;
-                    const unsigned char* from =
-                        live ? data + kv_off(c, pg, h, (at + row) & (c.page_tokens - 1)) + piece * 16 : data;
-                    cp_async16_to(ring + st * S::TILE + tile_at(row, piece), from, live ? 16 : 0);
+                    const int64_t o = __shfl_sync(0xffffffffu, off, p * ROWS >> 4);
+                    const unsigned char* from = data + o + row_off + (p * ROWS & 15) * c.token_stride;
+                    const uint32_t to = to0 + st * S::TILE + p * ROWS * 128;
+                    if (whole) {
+                        cp_async16_to(to, from);
+                    } else {
+                        const bool live = o >= 0 && at + r0 + p * ROWS < end;
+                        cp_async16_to(to, live ? from : data, live ? 16 : 0);
+                    }
                 }
                 asm volatile("cp.async.commit_group;\n" ::: "memory");
                 if (i >= AHEAD) {
@@ -437,6 +461,7 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
         const int mine = a.causal && qr < nrows ? min(end, sp.pos0 + qr / G + 1) : end;
         // No smaller than the least normal number: -inf times it stays -inf, and 2^(x 1e-38) is 1.
         const float log2s = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
+        const uint64_t log2s2 = pack2(log2s, log2s);
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         if (t == 0 || two) {
@@ -482,22 +507,25 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                     }
                 }
                 const float low = m == -INFINITY ? 0.0f : -m;
-                float sum[4] = {l, 0.0f, 0.0f, 0.0f};
+                const uint64_t low2 = pack2(low, low);
+                uint64_t sum[2] = {pack2(l, 0.0f), pack2(0.0f, 0.0f)};
 #pragma unroll
                 for (int part = 0; part < 4; ++part) {
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float x = s[32 * part + 2 * i], y = s[32 * part + 2 * i + 1];
-                        fma2(x, y, log2s, low);
+                        float x, y;
+                        unpack2(fma2(pack2(s[32 * part + 2 * i], s[32 * part + 2 * i + 1]), log2s2, low2), x, y);
                         x = exp2_fast(x);
                         y = exp2_fast(y);
-                        add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], x, y);
+                        sum[i & 1] = add2(sum[i & 1], pack2(x, y));
                         p[i] = bf16x2(x, y);
                     }
                     tmem_st16(s_at + 16 * part, p);
                 }
-                l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float l0, l1;
+                unpack2(add2(sum[0], sum[1]), l0, l1);
+                l = l0 + l1;
                 tmem_st_wait();
                 tc_before();
                 mbar_arrive(p_full + 8 * t);

@@ -131,8 +131,9 @@ def _p(t):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def nb_stride(n: int) -> int:
@@ -460,6 +461,7 @@ class KVCache:
                                       k.stride(2), strides[0], strides[1], strides[2], self.H, self.D,
                                       self.page_tokens, self.format)
         self._ref = ctypes.byref(self._struct)
+        self._device = k.get_device()   # -1: not on a GPU
 
     @classmethod
     def empty(cls, pages: int, H: int, D: int, page_tokens: int = 64, dtype=torch.int8, device="cuda"):
@@ -477,25 +479,27 @@ class KVCache:
 
 def _kv_here(cache: KVCache, *tensors):
     """Tensors of a cache call live on the cache's device, and that is the current one."""
-    dev = cache.k.device
+    dev = cache._device
     for t in tensors:
-        if t.device != dev:
+        if t.get_device() != dev:
             raise ValueError("the tensors of a call must be on the cache's device")
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError("the cache must be on the current CUDA device")
 
 
 def _kv_rows(cache: KVCache, table, cu, length, rows: int):
-    B = length.shape[0]
     if table.dtype != torch.int32 or cu.dtype != torch.int32 or length.dtype != torch.int32:
         raise TypeError("table, cu and length are int32")
-    if table.dim() != 2 or table.shape[0] != B or cu.shape != (B + 1,) or length.dim() != 1:
+    if length.dim() != 1 or cu.dim() != 1 or table.dim() != 2:
         raise ValueError("table is [B][pages], cu [B+1] and length [B]")
-    if not (cu.is_contiguous() and length.is_contiguous() and (table.shape[1] < 2 or table.stride(1) == 1)):
+    B, (table_rows, pages) = length.shape[0], table.shape
+    if table_rows != B or cu.shape[0] != B + 1:
+        raise ValueError("table is [B][pages], cu [B+1] and length [B]")
+    stride, step = table.stride()
+    if not (cu.is_contiguous() and length.is_contiguous() and (pages < 2 or step == 1)):
         raise ValueError("table rows, cu and length must be contiguous")
     _kv_here(cache, table, cu, length)
-    return ctypes.byref(_KvRowsStruct(table.data_ptr(), cu.data_ptr(), length.data_ptr(), table.stride(0), rows,
-                                      table.shape[1], B))
+    return ctypes.byref(_KvRowsStruct(table.data_ptr(), cu.data_ptr(), length.data_ptr(), stride, rows, pages, B))
 
 
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, cu: torch.Tensor,
@@ -505,14 +509,15 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tens
     int32 [B][pages], cu int32 [B+1], length int32 [B])."""
     if k.dtype not in _KEY_TYPES or v.dtype != k.dtype:
         raise TypeError("k and v are float32 or bfloat16")
-    if k.dim() != 3 or k.shape[1:] != (cache.H, cache.D) or v.shape != k.shape or v.stride() != k.stride():
+    shape, strides = k.shape, k.stride()
+    if len(shape) != 3 or shape[1] != cache.H or shape[2] != cache.D or v.shape != shape or v.stride() != strides:
         raise ValueError("k and v must be [rows][H][D] and share strides")
-    if k.stride(2) != 1:
+    if strides[2] != 1:
         raise ValueError("k and v must be contiguous along D")
-    rows = _kv_rows(cache, table, cu, length, k.shape[0])
+    rows = _kv_rows(cache, table, cu, length, shape[0])
     _kv_here(cache, k, v)
-    _check(lib().fathom_kv_write(cache._ref, rows, k.data_ptr(), v.data_ptr(), _KEY_TYPES[k.dtype], k.stride(0),
-                                 k.stride(1), _stream(stream)), "fathom_kv_write")
+    _check(lib().fathom_kv_write(cache._ref, rows, k.data_ptr(), v.data_ptr(), _KEY_TYPES[k.dtype], strides[0],
+                                 strides[1], _stream(stream)), "fathom_kv_write")
     return cache
 
 
@@ -521,22 +526,29 @@ def kv_read(cache: KVCache, table: torch.Tensor, cu: torch.Tensor, length: torch
     """Read the same rows back: (K, V), each [H][rows][D] in ``dtype`` (fp32
     or bf16), the layout ``pack`` takes.  ``out`` may give both tensors (any
     strides, channels contiguous), or None in the place of one not wanted."""
+    shape = (cache.H, rows, cache.D)
     if out is None:
-        out = tuple(torch.empty((cache.H, rows, cache.D), dtype=dtype, device=cache.k.device) for _ in range(2))
-    given = [t for t in out if t is not None]
-    for t in given:
-        if t.dtype not in _KEY_TYPES or t.dtype != given[0].dtype:
+        if dtype not in _KEY_TYPES:
             raise TypeError("K and V are read back in float32 or bfloat16")
-        if t.shape != (cache.H, rows, cache.D) or t.stride() != given[0].stride() or t.stride(2) != 1:
-            raise ValueError("out must be [H][rows][D] tensors of the same strides, contiguous along D")
-    if not given:
+        k, v = _new(cache.k, shape, dtype, stream), _new(cache.k, shape, dtype, stream)
+    else:
+        k, v = out
+    first = v if k is None else k
+    if first is None:
         raise ValueError("nothing to read")
+    strides = first.stride()
+    for t in (k, v):
+        if t is None:
+            continue
+        if t.dtype not in _KEY_TYPES or t.dtype != first.dtype:
+            raise TypeError("K and V are read back in float32 or bfloat16")
+        if t.shape != shape or t.stride() != strides or strides[2] != 1:
+            raise ValueError("out must be [H][rows][D] tensors of the same strides, contiguous along D")
+        _kv_here(cache, t)
     w = _kv_rows(cache, table, cu, length, rows)
-    _kv_here(cache, *given)
-    _check(lib().fathom_kv_read(cache._ref, w, *(None if t is None else t.data_ptr() for t in out),
-                                _KEY_TYPES[given[0].dtype], given[0].stride(0), given[0].stride(1), _stream(stream)),
-           "fathom_kv_read")
-    return tuple(out)
+    _check(lib().fathom_kv_read(cache._ref, w, None if k is None else k.data_ptr(), None if v is None else v.data_ptr(),
+                                _KEY_TYPES[first.dtype], strides[0], strides[1], _stream(stream)), "fathom_kv_read")
+    return k, v
 
 
 def paged_attention_workspace_bytes(H: int, G: int, D: int, rows: int, B: int, max_new: int, max_len: int,
@@ -544,11 +556,19 @@ def paged_attention_workspace_bytes(H: int, G: int, D: int, rows: int, B: int, m
     return int(lib().fathom_paged_attention_workspace_bytes(H, G, D, rows, B, max_new, max_len, _KEY_TYPES[dtype]))
 
 
-def _workspace(workspace, need: int, device):
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+def _new(like, shape, dtype, stream):
+    """A tensor for a call's own use or result.  The call may be on another
+    stream than the current one, which the memory belongs to."""
+    t = like.new_empty(shape, dtype=dtype)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _workspace(workspace, need: int, like, stream):
     if workspace is None:
-        return None, None, 0
+        workspace = _new(like, need, torch.uint8, stream) if need else None
+        return workspace, None if workspace is None else workspace.data_ptr(), need
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -559,23 +579,24 @@ def paged_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, cu: to
     head h*G + g belongs to KV head h) over its cached tokens, the rows' own
     among them: a prompt chunk or single tokens.  ``max_new`` and
     ``max_len`` bound the batch's rows and lengths.  Returns [rows][H*G][D]."""
-    if q.dtype not in _KEY_TYPES:
+    dt = _KEY_TYPES.get(q.dtype)
+    if dt is None:
         raise TypeError("q is float32 or bfloat16")
-    if q.dim() != 3 or q.shape[2] != cache.D or q.shape[1] % cache.H or q.stride(2) != 1:
+    shape, strides = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != cache.D or shape[1] % cache.H or strides[2] != 1:
         raise ValueError("q must be [rows][H*G][D], contiguous along D")
-    rows, G = q.shape[0], q.shape[1] // cache.H
+    rows, G = shape[0], shape[1] // cache.H
     if out is None:
-        out = torch.empty((rows, q.shape[1], cache.D), dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        out = _new(q, shape, q.dtype, stream)
+    elif out.dtype != q.dtype or out.shape != shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous [rows][H*G][D] tensor of q's type")
     w = _kv_rows(cache, table, cu, length, rows)
     _kv_here(cache, q, out)
-    B, dt = length.shape[0], _KEY_TYPES[q.dtype]
     L = lib()
-    need = L.fathom_paged_attention_workspace_bytes(cache.H, G, cache.D, rows, B, max_new, max_len, dt)
-    workspace, ws, ws_bytes = _workspace(workspace, need, q.device)
+    need = L.fathom_paged_attention_workspace_bytes(cache.H, G, cache.D, rows, length.shape[0], max_new, max_len, dt)
+    workspace, ws, ws_bytes = _workspace(workspace, need, q, stream)
     sc = cache.D ** -0.5 if scale is None else float(scale)
-    _check(L.fathom_paged_attention(cache._ref, w, q.data_ptr(), dt, q.stride(0), q.stride(1), G, max_new, max_len,
+    _check(L.fathom_paged_attention(cache._ref, w, q.data_ptr(), dt, strides[0], strides[1], G, max_new, max_len,
                                     int(causal), sc, out.data_ptr(), ws, ws_bytes, _stream(stream)),
            "fathom_paged_attention")
     return out
@@ -587,23 +608,27 @@ def paged_union_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, 
     """``union_attention`` with the winners' rows taken from one sequence of
     the paged cache: q fp32 [H][G][D], table int32 [pages] (or [1][pages]),
     n tokens.  Returns fp32 [H][G][D]."""
-    table = table.reshape(-1)
-    if q.dtype != torch.float32 or q.dim() != 3 or q.shape[0] != cache.H or q.shape[2] != cache.D or not q.is_contiguous():
+    if table.dim() == 2 and table.shape[0] == 1:
+        table = table[0]
+    shape = q.shape
+    if q.dtype != torch.float32 or len(shape) != 3 or shape[0] != cache.H or shape[2] != cache.D or not q.is_contiguous():
         raise ValueError("q must be a contiguous fp32 [H][G][D] tensor")
     if table.dtype != torch.int32 or union_idx.dtype != torch.int32 or union_count.dtype != torch.int32:
         raise TypeError("table, union_idx and union_count are int32")
-    if union_idx.dim() != 2 or union_idx.shape[0] != cache.H or union_count.shape != (cache.H,) or \
-            not (union_idx.is_contiguous() and union_count.is_contiguous() and table.is_contiguous()):
+    if union_idx.dim() != 2 or union_idx.shape[0] != cache.H or union_count.dim() != 1 or union_count.shape[0] != cache.H or \
+            not (union_idx.is_contiguous() and union_count.is_contiguous()):
         raise ValueError("union_idx must be [H][M] and union_count [H], as topk writes them")
-    G, M = q.shape[1], union_idx.shape[1]
+    if table.dim() != 1 or not table.is_contiguous():
+        raise ValueError("table must be the contiguous [pages] of one sequence")
+    G, M = shape[1], union_idx.shape[1]
     if out is None:
-        out = torch.empty_like(q)
-    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        out = _new(q, shape, q.dtype, stream)
+    elif out.dtype != q.dtype or out.shape != shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous fp32 [H][G][D] tensor")
     _kv_here(cache, q, table, union_idx, union_count, out)
     L = lib()
     workspace, ws, ws_bytes = _workspace(
-        workspace, L.fathom_paged_union_attention_workspace_bytes(cache.H, G, cache.D, M), q.device)
+        workspace, L.fathom_paged_union_attention_workspace_bytes(cache.H, G, cache.D, M), q, stream)
     sc = cache.D ** -0.5 if scale is None else float(scale)
     _check(L.fathom_paged_union_attention(cache._ref, table.data_ptr(), table.numel(), n, q.data_ptr(), G,
                                           union_idx.data_ptr(), union_count.data_ptr(), M, sc, out.data_ptr(), ws,
