@@ -198,10 +198,11 @@ __device__ __forceinline__ int64_t chunk_off(const KvCache& c, int page, int at,
     return page < 0 ? -1 : kv_off(c, page, h, (at + 16 * lane) & (c.page_tokens - 1));
 }
 
-// The whole 128-token tiles of K and V from `begin` on, in the order K0 V0 K1 V1 ..., into the ring.
+// The whole 128-token tiles of K and V from `begin` on, in the order K0 V0 K1 V1 ..., into the ring.  Q's copies
+// are on their way already: `q_full` is told when they have come.
 template <int D, int FMT>
 __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* table, int table_pages, int h, int begin, int end,
-                                           uint32_t ring, uint32_t full, uint32_t empty)
+                                           uint32_t ring, uint32_t full, uint32_t empty, uint32_t q_full)
 {
     using S = ChunkShape<D>;
     const int t = threadIdx.x & 127, lane = threadIdx.x & 31;
@@ -241,6 +242,7 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
                 if (i >= AHEAD) {
                     asm volatile("cp.async.wait_group %0;\n" ::"n"(AHEAD) : "memory");
                     fence_async_smem();
+                    if (i == AHEAD) mbar_arrive(q_full);
                     mbar_arrive(full + 8 * ((i - AHEAD) % S::STAGES));
                 }
             }
@@ -248,6 +250,7 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
         }
         cp_async_wait_all();
         fence_async_smem();
+        if (i <= AHEAD) mbar_arrive(q_full);
         if (ok)
             for (int k = max(0, i - AHEAD); k < i; ++k) mbar_arrive(full + 8 * (k % S::STAGES));
     } else {
@@ -274,6 +277,9 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
         };
         int i = 0;
         if (tiles > 0) fetch(begin, false);
+        cp_async_wait_all();
+        fence_async_smem();
+        mbar_arrive(q_full);
         for (int j = 0; j < tiles && ok; ++j) {
             const int at = begin + j * kChunkKeys;
             next = chunk_page(c, table, table_pages, at + kChunkKeys, end, lane);
@@ -322,9 +328,9 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const uint32_t q_s = smem_addr(base), ring = q_s + S::QB, bars = q_s + static_cast<uint32_t>(S::BARS);
-    const uint32_t full = bars, empty = bars + 8 * ST, s_full = bars + 16 * ST, p_full = s_full + 16, o_full = p_full + 16,
+    const uint32_t full = bars, empty = bars + 8 * ST, s_full = bars + 16 * ST, p_full = s_full + 16, o_full = p_full + 32,
                    q_full = o_full + 16, drain = q_full + 8, tmem_slot = drain + 8;
-    static_assert(16 * ST + 16 * 3 + 8 * 2 + 4 <= 256, "barriers fit their space");
+    static_assert(16 * ST + 16 * 4 + 8 * 2 + 4 <= 256, "barriers fit their space");
 
     const KvAttend& a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -351,7 +357,8 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(s_full + 8 * i, 1);
-                mbar_init(p_full + 8 * i, 128);
+                mbar_init(p_full + 8 * i, 128);        // the first half of the weights
+                mbar_init(p_full + 16 + 8 * i, 128);   // and the second
                 mbar_init(o_full + 8 * i, 1);
             }
             mbar_init(q_full, 128);
@@ -378,9 +385,9 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                 }
                 tc_commit(s_full + 8 * t);
             };
-            auto values = [&](int t, int st, bool add) {
+            auto values = [&](int t, int st, int half, bool add) {
 #pragma unroll
-                for (int ks = 0; ks < kChunkKeys / 16; ++ks)
+                for (int ks = half * kChunkKeys / 32; ks < (half + 1) * kChunkKeys / 32; ++ks)
                     tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * ks,
                               tc_operand(ring + st * S::TILE + ks * 2048, kChunkKeys * 128), shape_o, add || ks > 0);
             };
@@ -396,10 +403,14 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                 const bool more = j + 1 < tiles;
                 ok = mbar_wait(full + 8 * (iv % ST), (iv / ST) & 1);
                 for (int t = 0; t < nt && ok; ++t) {
-                    ok = mbar_wait(p_full + 8 * t, j & 1);
+                    for (int half = 0; half < 2 && ok; ++half) {
+                        ok = mbar_wait(p_full + 16 * half + 8 * t, j & 1);
+                        if (!ok) break;
+                        tc_after();
+                        if (half == 0) values(t, iv % ST, 0, j > 0);
+                        else values(t, iv % ST, 1, true);
+                    }
                     if (!ok) break;
-                    tc_after();
-                    values(t, iv % ST, j > 0);
                     if (!more) tc_commit(o_full + 8 * t);
                     if (t == nt - 1) tc_commit(empty + 8 * (iv % ST));
                     if (more) {
@@ -422,35 +433,30 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
             constexpr int PIECES = D / 8, ROWS = 128 / PIECES;
             const int t = threadIdx.x & 127, piece = t % PIECES, at_row = t / PIECES;
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-            const bool vec = ((reinterpret_cast<uintptr_t>(q) & 15) | (a.q_tok & 7) | (a.q_head & 7)) == 0;
             const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // the softmax uses |scale|
+            const bool vec = flip == 0 && ((reinterpret_cast<uintptr_t>(q) & 15) | (a.q_tok & 7) | (a.q_head & 7)) == 0;
             for (int row = at_row; row < kChunkRows; row += ROWS) {
                 const int qr = r0 + row;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (qr < nrows) {
-                    const __nv_bfloat16* from =
-                        q + (sp.first + qr / G) * a.q_tok + (static_cast<int64_t>(h) * G + qr % G) * a.q_head + piece * 8;
-                    if (vec) {
-                        x = __ldg(reinterpret_cast<const uint4*>(from));
-                    } else {
-                        uint32_t w[4];
+                const uint32_t to = q_s + (row >> 7) * S::TILE + tile_at(row & 127, piece);
+                const __nv_bfloat16* from = q;
+                if (qr < nrows)
+                    from += (sp.first + qr / G) * a.q_tok + (static_cast<int64_t>(h) * G + qr % G) * a.q_head + piece * 8;
+                if (vec) {
+                    cp_async16_to(to, from, qr < nrows ? 16 : 0);
+                } else {
+                    uint32_t w[4] = {0, 0, 0, 0};
+                    if (qr < nrows) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            w[i] = __bfloat16_as_ushort(from[2 * i]) |
-                                   static_cast<uint32_t>(__bfloat16_as_ushort(from[2 * i + 1])) << 16;
-                        x = make_uint4(w[0], w[1], w[2], w[3]);
+                            w[i] = (__bfloat16_as_ushort(from[2 * i]) |
+                                    static_cast<uint32_t>(__bfloat16_as_ushort(from[2 * i + 1])) << 16) ^ flip;
                     }
-                    x.x ^= flip;
-                    x.y ^= flip;
-                    x.z ^= flip;
-                    x.w ^= flip;
+                    st_shared16(to, make_uint4(w[0], w[1], w[2], w[3]));
                 }
-                st_shared16(q_s + (row >> 7) * S::TILE + tile_at(row & 127, piece), x);
             }
-            fence_async_smem();
-            mbar_arrive(q_full);
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
         }
-        if (!chunk_load<D, FMT>(a.c, table, a.w.table_pages, h, begin, end, ring, full, empty)) atomicOr(fault, kFaultTimeout);
+        if (!chunk_load<D, FMT>(a.c, table, a.w.table_pages, h, begin, end, ring, full, empty, q_full)) atomicOr(fault, kFaultTimeout);
     } else {
         regs_up<kRegsSoftmax>();
         const int t = warp >> 2;
@@ -522,13 +528,15 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                         p[i] = bf16x2(x, y);
                     }
                     tmem_st16(s_at + 16 * part, p);
+                    if (part & 1) {
+                        tmem_st_wait();
+                        tc_before();
+                        mbar_arrive(p_full + 8 * (part - 1) + 8 * t);
+                    }
                 }
                 float l0, l1;
                 unpack2(add2(sum[0], sum[1]), l0, l1);
                 l = l0 + l1;
-                tmem_st_wait();
-                tc_before();
-                mbar_arrive(p_full + 8 * t);
             }
             if (ok && tiles > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait(o_full + 8 * t, 0));
