@@ -114,8 +114,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r)
 // where the product runs along the rows (V).
 __device__ __forceinline__ uint64_t tc_operand(uint32_t smem_at, uint32_t lbo)
 {
-    return (static_cast<uint64_t>(2) << 61) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(1024 >> 4) << 32) |
-           (static_cast<uint64_t>(lbo >> 4) << 16) | ((smem_at & 0x3ffff) >> 4);
+    constexpr uint32_t hi = (2u << 29) | (1u << 14) | (1024 >> 4);
+    return static_cast<uint64_t>(hi) << 32 | (((lbo >> 4) << 16) + (smem_at >> 4));
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
 }
 
 // bf16 x bf16 -> fp32, 128 rows, N columns; `along_rows`: B is stored [k][n].
@@ -333,7 +341,8 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
     static_assert(16 * ST + 16 * 4 + 8 * 2 + 4 <= 256, "barriers fit their space");
 
     const KvAttend& a = g.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the same in all lanes, as the compiler can tell
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int h = blockIdx.y, b = blockIdx.z, G = a.G;
     // Later rows see more tokens: they start first.
     const int tile = g.s.row_tiles - 1 - static_cast<int>(blockIdx.x % g.s.row_tiles), split = blockIdx.x / g.s.row_tiles;
@@ -374,57 +383,70 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
 
     if (warp >= 12) {
         regs_down<kRegsIssue>();
-        if (warp == 12 && lane == 0 && tiles > 0) {
+        if (warp == 12 && tiles > 0) {
+            // The whole warp goes along, so that operands are in uniform registers; one lane issues.  (A lane on its own
+            // took 90 cycles to a product, more than the product.)
             constexpr uint32_t shape_s = tc_shape(kChunkKeys, false), shape_o = tc_shape(D, true);
             auto scores = [&](int t, int st) {
+                const uint64_t q = tc_operand(q_s + t * S::TILE, 0), k = tc_operand(ring + st * S::TILE, 0);
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * (kChunkKeys * 128) + (ks & 3) * 32;
-                    tc_mma_ss(tmem + 128 * t, tc_operand(q_s + t * S::TILE + off, 0), tc_operand(ring + st * S::TILE + off, 0),
-                              shape_s, ks > 0);
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * (kChunkKeys * 128) + (ks & 3) * 32) >> 4;
+                        tc_mma_ss(tmem + 128 * t, q + off, k + off, shape_s, ks > 0);
+                    }
+                    tc_commit(s_full + 8 * t);
                 }
-                tc_commit(s_full + 8 * t);
+                __syncwarp();
             };
             auto values = [&](int t, int st, int half, bool add) {
+                const uint64_t v = tc_operand(ring + st * S::TILE + half * (kChunkKeys / 2) * 128, kChunkKeys * 128);
+                const uint32_t p = tmem + 128 * t + half * (kChunkKeys / 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = half * kChunkKeys / 32; ks < (half + 1) * kChunkKeys / 32; ++ks)
-                    tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * ks,
-                              tc_operand(ring + st * S::TILE + ks * 2048, kChunkKeys * 128), shape_o, add || ks > 0);
+                    for (int ks = 0; ks < kChunkKeys / 32; ++ks)
+                        tc_mma_ts(tmem + 256 + 128 * t, p + 8 * ks, v + ks * (2048 >> 4), shape_o, add || ks > 0);
+                }
+                __syncwarp();
             };
+            auto done = [&](uint32_t bar) {
+                if (elect_one()) tc_commit(bar);
+                __syncwarp();
+            };
+            auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
             const int nt = two ? 2 : 1;
-            bool ok = mbar_wait(q_full, 0) && mbar_wait(full, 0);
+            bool ok = wait(q_full, 0) && wait(full, 0);
             if (ok) {
                 tc_after();
                 for (int t = 0; t < nt; ++t) scores(t, 0);
-                tc_commit(empty);
+                done(empty);
             }
             for (int j = 0; j < tiles && ok; ++j) {
                 const int iv = 2 * j + 1, ik = iv + 1;
                 const bool more = j + 1 < tiles;
-                ok = mbar_wait(full + 8 * (iv % ST), (iv / ST) & 1);
+                ok = wait(full + 8 * (iv % ST), (iv / ST) & 1);
                 for (int t = 0; t < nt && ok; ++t) {
                     for (int half = 0; half < 2 && ok; ++half) {
-                        ok = mbar_wait(p_full + 16 * half + 8 * t, j & 1);
+                        ok = wait(p_full + 16 * half + 8 * t, j & 1);
                         if (!ok) break;
                         tc_after();
-                        if (half == 0) values(t, iv % ST, 0, j > 0);
-                        else values(t, iv % ST, 1, true);
+                        values(t, iv % ST, half, j > 0 || half > 0);
                     }
                     if (!ok) break;
-                    if (!more) tc_commit(o_full + 8 * t);
-                    if (t == nt - 1) tc_commit(empty + 8 * (iv % ST));
+                    if (!more) done(o_full + 8 * t);
+                    if (t == nt - 1) done(empty + 8 * (iv % ST));
                     if (more) {
-                        if (t == 0) ok = mbar_wait(full + 8 * (ik % ST), (ik / ST) & 1);
+                        if (t == 0) ok = wait(full + 8 * (ik % ST), (ik / ST) & 1);
                         if (!ok) break;
                         scores(t, ik % ST);
                     }
                 }
-                if (ok && more) tc_commit(empty + 8 * (ik % ST));
+                if (ok && more) done(empty + 8 * (ik % ST));
             }
-            if (!ok) atomicOr(fault, kFaultTimeout);
             // Nothing is on its way in tensor memory when it is freed.
-            tc_commit(drain);
-            if (!mbar_wait(drain, 0)) atomicOr(fault, kFaultTimeout);
+            done(drain);
+            if (!wait(drain, 0)) ok = false;
+            if (!ok && lane == 0) atomicOr(fault, kFaultTimeout);
         }
         __syncwarp();
     } else if (warp >= 8) {
