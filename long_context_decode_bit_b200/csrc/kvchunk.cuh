@@ -15,8 +15,8 @@
 // Both operands are kept with 64 channels (128 bytes) to a row and the
 // 128-byte swizzle, K read along the channels and V along the tokens from the
 // same layout.  16-bit pages are copied there by cp.async, 16 bytes a thread,
-// zeros for tokens that are not there; 8-bit pages are decoded to bf16 on the
-// way (once for 256 query rows), their next tile already in registers.
+// zeros for tokens that are not there; 8-bit pages are copied beside them, by
+// the threads that then decode them to bf16 (once for 256 query rows).
 //
 // The running maximum m of a row is raised only when it grew by more than
 // 2^8 (P and l then stay below 2^8 times what the true maximum gives, far
@@ -40,13 +40,16 @@ constexpr int kChunkKeys = 128;   // tokens of a tile
 constexpr int kRegsSoftmax = 192, kRegsLoad = 80, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 512, "more registers than the block has");
 
-template <int D>
+template <int D, int FMT>
 struct ChunkShape {
+    static constexpr bool CODED = FMT != FATHOM_KV_BF16;
     static constexpr int DB = D / 64;                             // 64-channel blocks of a row
     static constexpr int TILE = kChunkKeys * 128 * DB;            // bytes of 128 rows
-    static constexpr int STAGES = D == 128 ? 5 : 8;               // tiles of K or V held
+    static constexpr int STAGES = D == 128 ? (CODED ? 3 : 5) : (CODED ? 6 : 8);   // tiles of K or V held as operands
+    static constexpr int RAWS = CODED ? (D == 128 ? 3 : 4) : 0;   // and as they come
+    static constexpr int RAW = kChunkKeys * D + 2048;             // codes, and exponents in 16 bytes a thread
     static constexpr int QB = 2 * TILE;
-    static constexpr size_t BARS = QB + static_cast<size_t>(STAGES) * TILE;
+    static constexpr size_t BARS = QB + static_cast<size_t>(STAGES) * TILE + static_cast<size_t>(RAWS) * RAW;
     static constexpr size_t SMEM = BARS + 256 + 1024;             // the base is moved up to a multiple of 1024
 };
 
@@ -212,11 +215,11 @@ template <int D, int FMT>
 __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* table, int table_pages, int h, int begin, int end,
                                            uint32_t ring, uint32_t full, uint32_t empty, uint32_t q_full)
 {
-    using S = ChunkShape<D>;
+    using S = ChunkShape<D, FMT>;
     const int t = threadIdx.x & 127, lane = threadIdx.x & 31;
     const int tiles = (end - begin + kChunkKeys - 1) / kChunkKeys;
     bool ok = true;
-    int page = chunk_page(c, table, table_pages, begin, end, lane), next = -1;
+    int page = chunk_page(c, table, table_pages, begin, end, lane);
     if constexpr (FMT == FATHOM_KV_BF16) {
         constexpr int PIECES = D / 8, ROWS = 128 / PIECES;   // rows of a pass
         constexpr int AHEAD = S::STAGES - 2;                 // stages that may be on their way
@@ -228,7 +231,7 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
             const int at = begin + j * kChunkKeys;
             const int64_t off = chunk_off(c, page, at, h, lane);
             const bool whole = end - at >= kChunkKeys && __ballot_sync(0xffffffffu, page >= 0) == 0xff;
-            next = chunk_page(c, table, table_pages, at + kChunkKeys, end, lane);
+            page = chunk_page(c, table, table_pages, at + kChunkKeys, end, lane);
             for (int s = 0; s < 2; ++s, ++i) {
                 const int st = i % S::STAGES;
                 ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((i / S::STAGES) & 1) ^ 1));
@@ -254,7 +257,6 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
                     mbar_arrive(full + 8 * ((i - AHEAD) % S::STAGES));
                 }
             }
-            page = next;
         }
         cp_async_wait_all();
         fence_async_smem();
@@ -262,66 +264,85 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
         if (ok)
             for (int k = max(0, i - AHEAD); k < i; ++k) mbar_arrive(full + 8 * (k % S::STAGES));
     } else {
-        constexpr int PIECES = D / 16, ROWS = 128 / PIECES, N = 128 / ROWS;   // 16 codes to a piece
-        const int piece = t % PIECES, r0 = t / PIECES;
+        // A thread copies 16-code pieces lq, lq + 4 of the rows lr, lr + 32, lr + 64, lr + 96 to a place of its own
+        // some tiles ahead, and decodes those same pieces from there.
+        constexpr int KP = D / 64, AHEAD = S::RAWS - 1;
+        const int lr = t >> 2, lq = t & 3, group = lr >> 4;
         const CodeMasks masks = code_masks<FMT>();
-        uint4 raw[N];
-        uint32_t pw[N];
-        auto fetch = [&](int at, bool v) {
-            const unsigned char* data = v ? c.v : c.k;
-            const unsigned char* sc = v ? c.vs : c.ks;
+        const uint32_t mine = ring + S::STAGES * S::TILE + t * 16;
+        const int64_t row_off = (lr & 15) * c.token_stride + lq * 16;
+        const int64_t row_soff = (lr & 15) * c.stoken_stride + (D == 64 ? lq >> 1 : 0);
+        const int stages = 2 * tiles;
+        int is = 0, at = begin;
+        int64_t off = -1, soff = 0;
+        uint32_t sc[4] = {0, 0, 0, 0};   // exponent bytes on their way
+        auto issue = [&]() {
+            const uint32_t slot = mine + (is % S::RAWS) * S::RAW;
+            if (is > 0)
+                st_shared16(mine + ((is - 1) % S::RAWS) * S::RAW + 4 * KP * 2048, make_uint4(sc[0], sc[1], sc[2], sc[3]));
+            if (is < stages) {
+                if ((is & 1) == 0) {
+                    at = begin + (is >> 1) * kChunkKeys;
+                    off = chunk_off(c, page, at, h, lane);
+                    soff = page < 0 ? 0 : kv_scale_off(c, page, h, (at + 16 * lane) & (c.page_tokens - 1));
+                    page = chunk_page(c, table, table_pages, at + kChunkKeys, end, lane);
+                }
+                const unsigned char* data = (is & 1) ? c.v : c.k;
+                const unsigned char* scale = (is & 1) ? c.vs : c.ks;
 #pragma unroll
-            for (int p = 0; p < N; ++p) {
-                const int row = r0 + p * ROWS;
-                const int pg = __shfl_sync(0xffffffffu, page, row >> 4);
-                raw[p] = make_uint4(0, 0, 0, 0);
-                pw[p] = 0;
-                if (pg >= 0 && at + row < end) {
-                    const int tok = (at + row) & (c.page_tokens - 1);
-                    raw[p] = __ldg(reinterpret_cast<const uint4*>(data + kv_off(c, pg, h, tok) + piece * 16));
-                    pw[p] = __ldg(sc + kv_scale_off(c, pg, h, tok) + (piece >> 1));
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t o = __shfl_sync(0xffffffffu, off, group + 2 * i), so = __shfl_sync(0xffffffffu, soff, group + 2 * i);
+                    const bool live = o >= 0 && at + lr + 32 * i < end;
+                    const unsigned char* from = live ? data + o + row_off : data;
+#pragma unroll
+                    for (int k = 0; k < KP; ++k) cp_async16_to(slot + (i * KP + k) * 2048, from + 64 * k, live ? 16 : 0);
+                    sc[i] = 0;
+                    if (live) {
+                        const unsigned char* sp = scale + so + row_soff;
+                        sc[i] = D == 128 ? __ldg(reinterpret_cast<const uint32_t*>(sp)) : __ldg(sp);
+                    }
                 }
             }
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
+            ++is;
         };
+        for (int i = 0; i < AHEAD; ++i) issue();
         int i = 0;
-        if (tiles > 0) fetch(begin, false);
-        cp_async_wait_all();
-        fence_async_smem();
-        mbar_arrive(q_full);
-        for (int j = 0; j < tiles && ok; ++j) {
-            const int at = begin + j * kChunkKeys;
-            next = chunk_page(c, table, table_pages, at + kChunkKeys, end, lane);
-#pragma unroll
-            for (int s = 0; s < 2; ++s, ++i) {
-                const int st = i % S::STAGES;
-                ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((i / S::STAGES) & 1) ^ 1));
-                if (!ok) break;
-#pragma unroll
-                for (int p = 0; p < N; ++p) {
-                    const int row = r0 + p * ROWS;
-                    const uint32_t f = pow_bits<FMT>(pw[p]) * 0x10001u;
-                    const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
-                    uint4 o[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        o[k] = make_uint4(decode2<FMT, 0, 1>(w[2 * k], w[2 * k], f, masks), decode2<FMT, 2, 3>(w[2 * k], w[2 * k], f, masks),
-                                          decode2<FMT, 0, 1>(w[2 * k + 1], w[2 * k + 1], f, masks),
-                                          decode2<FMT, 2, 3>(w[2 * k + 1], w[2 * k + 1], f, masks));
-                    // half of the threads store their second piece first: 8 threads then fill all banks once
-                    const int first = (piece >> 2) & 1;
-                    const uint32_t to = ring + st * S::TILE;
-                    st_shared16(to + tile_at(row, 2 * piece + first), first ? o[1] : o[0]);
-                    st_shared16(to + tile_at(row, 2 * piece + 1 - first), first ? o[0] : o[1]);
-                }
-                if (s == 0) {
-                    fetch(at, true);
-                } else {
-                    page = next;
-                    if (j + 1 < tiles) fetch(at + kChunkKeys, false);
-                }
+        for (; i < stages && ok; ++i) {
+            asm volatile("cp.async.wait_group %0;\n" ::"n"(AHEAD - 1) : "memory");
+            if (i == 0) {
                 fence_async_smem();
-                mbar_arrive(full + 8 * st);
+                mbar_arrive(q_full);
             }
+            issue();
+            const int st = i % S::STAGES;
+            ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((i / S::STAGES) & 1) ^ 1));
+            if (!ok) break;
+            const uint32_t from = mine + (i % S::RAWS) * S::RAW, to = ring + st * S::TILE + tile_at(lr, 2 * lq);
+            uint32_t ps[4];
+            lds_words<4>(from + 4 * KP * 2048, ps);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    uint32_t w[4];
+                    lds_words<4>(from + (r * KP + k) * 2048, w);
+                    const uint32_t byte = D == 128 ? (ps[r] >> (16 * k + 8 * (lq >> 1))) & 0xff : ps[r];
+                    const uint32_t f = pow_bits<FMT>(byte) * 0x10001u;
+                    // the row's two 16-byte pieces, the second one chunk on in the swizzle
+                    const uint32_t there = to + r * 32 * 128 + k * (kChunkKeys * 128);
+                    st_shared16(there, make_uint4(decode2<FMT, 0, 1>(w[0], w[0], f, masks), decode2<FMT, 2, 3>(w[0], w[0], f, masks),
+                                                  decode2<FMT, 0, 1>(w[1], w[1], f, masks), decode2<FMT, 2, 3>(w[1], w[1], f, masks)));
+                    st_shared16(there ^ 16, make_uint4(decode2<FMT, 0, 1>(w[2], w[2], f, masks), decode2<FMT, 2, 3>(w[2], w[2], f, masks),
+                                                       decode2<FMT, 0, 1>(w[3], w[3], f, masks), decode2<FMT, 2, 3>(w[3], w[3], f, masks)));
+                }
+            fence_async_smem();
+            mbar_arrive(full + 8 * st);
+        }
+        cp_async_wait_all();
+        if (stages == 0) {
+            fence_async_smem();
+            mbar_arrive(q_full);
         }
     }
     return ok;
@@ -331,7 +352,7 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(kChunkThreads, 1)
 kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
 {
-    using S = ChunkShape<D>;
+    using S = ChunkShape<D, FMT>;
     constexpr int ST = S::STAGES;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
@@ -620,7 +641,7 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
 template <int D, int FMT>
 int launch_chunk_t(const KvRowsArgs& g, cudaStream_t stream)
 {
-    using S = ChunkShape<D>;
+    using S = ChunkShape<D, FMT>;
     const void* f = reinterpret_cast<const void*>(kv_chunk_kernel<D, FMT>);
     // The roles' registers must add up to no more than the block is launched with, or the softmax waits for ever.
     static const int launch_regs = [f] {
