@@ -12,49 +12,53 @@ constexpr int kSms = 148;        // the machine this library is written for; onl
 
 int64_t round_up(int64_t x, int64_t to) { return ceil_div(x, to) * to; }
 
-// Tiles of kChunkRows query rows, one CTA to an SM.  The cut into stretches
-// that ends soonest: waves of CTAs times a stretch's tiles of tokens (and
-// about three tiles' time to start and end a CTA).
-KvSplit chunk_split(int H, int G, int64_t rows, int B, int64_t qrows, int64_t max_len)
+// The cut of `tiles` tiles of tokens into stretches that ends soonest: waves of
+// CTAs (`at_once` to the machine) times a stretch's tiles (`us` each, and the
+// time of `start` of them to begin and end a CTA), and writing and joining the
+// stretches' sums.  A batch's longest sequence is `longest` of the `items`;
+// the others are taken to be half as long, since only the device knows.
+// Returns the tiles of a stretch.
+int64_t cut(int64_t tiles, int64_t items, int64_t longest, int64_t heads, int D, int64_t at_once, double us, int64_t start)
 {
-    KvSplit s{};
-    s.tile_rows = kChunkRows;
-    s.row_tiles = static_cast<int32_t>(ceil_div(qrows, kChunkRows));
-    // Sequences of a batch are uneven: no more row tiles than all its rows fill, and one begun by each sequence.
-    const int64_t items = H * std::min(static_cast<int64_t>(B) * s.row_tiles, ceil_div(rows * G, kChunkRows) + B - 1);
-    const int64_t tiles = std::max<int64_t>(1, ceil_div(max_len, kChunkKeys));
-    int64_t best = 0, each = tiles;
+    double best = 0.0;
+    int64_t each = tiles;
     for (int64_t n = 1; n <= 32 && n <= tiles; ++n) {
-        const int64_t len = ceil_div(tiles, n), cost = ceil_div(items * n, kSms) * (len + 3 + (n > 1 ? 1 : 0));
+        const int64_t len = ceil_div(tiles, n);
+        const int64_t waves = ceil_div(longest * n + (items - longest) * ceil_div(n, 2), at_once);
+        const double cost = waves * (len + start) * us + (n > 1 ? 4.0 + static_cast<double>(n) * heads * D * 8 / 5e6 : 0.0);
         if (n == 1 || cost < best) {
             best = cost;
             each = len;
         }
     }
-    s.chunk = static_cast<int32_t>(each * kChunkKeys);
-    s.splits = static_cast<int32_t>(ceil_div(tiles, each));
-    return s;
+    return each;
 }
 
-// Tiles of 8*nt query rows by stretches of tokens.  A CTA's four warps want
-// 64 tokens at least each; four CTAs fit an SM.
+// How rows of queries and tokens are cut into CTAs.
 KvSplit rows_split(int H, int G, int D, int64_t rows, int B, int64_t max_new, int64_t max_len, int q_dtype)
 {
     KvSplit s{};
-    const int64_t qrows = max_new * G;
-    if (q_dtype == FATHOM_KEYS_BF16 && (D == 64 || D == 128) && qrows > 64) return chunk_split(H, G, rows, B, qrows, max_len);
-    s.nt = qrows <= 8 ? 1 : (D <= 128 ? 4 : 2);
-    s.tile_rows = 8 * s.nt;
+    const int64_t qrows = max_new * G, len = std::max<int64_t>(max_len, 1);
+    const bool chunk = q_dtype == FATHOM_KEYS_BF16 && (D == 64 || D == 128) && qrows > 64;
+    s.nt = chunk ? 0 : (qrows <= 8 ? 1 : (D <= 128 ? 4 : 2));
+    s.tile_rows = chunk ? kChunkRows : 8 * s.nt;
     s.row_tiles = static_cast<int32_t>(ceil_div(qrows, s.tile_rows));
-    const int64_t items = static_cast<int64_t>(B) * H * s.row_tiles;
-    // One session: its stretches are equal, one wave of CTAs.  Several of uneven
-    // lengths: shorter stretches, so that the longest session does not end alone.
-    const int64_t want = B == 1 ? 4 * kSms : 32 * kSms;
-    const int64_t splits = std::max<int64_t>(1, want / items);
-    int64_t chunk = round_up(ceil_div(std::max<int64_t>(max_len, 1), splits), 64);
-    if (chunk < 256) chunk = 256;
-    s.chunk = static_cast<int32_t>(chunk);
-    s.splits = static_cast<int32_t>(ceil_div(std::max<int64_t>(max_len, 1), chunk));
+    if (s.nt == 1) {
+        // Single tokens.  Four CTAs fit an SM.  One session: its stretches are equal, one wave of CTAs.  Several of
+        // uneven lengths: shorter stretches, so that the longest session does not end alone.
+        const int64_t items = static_cast<int64_t>(B) * H, want = B == 1 ? 4 * kSms : 32 * kSms;
+        const int64_t splits = std::max<int64_t>(1, want / items);
+        s.chunk = static_cast<int32_t>(std::max<int64_t>(round_up(ceil_div(len, splits), 64), 256));
+    } else {
+        // A batch has no more row tiles than all its rows fill, and one begun by each sequence.
+        const int64_t items = H * std::min(static_cast<int64_t>(B) * s.row_tiles, ceil_div(rows * G, s.tile_rows) + B - 1);
+        const int64_t longest = std::min(items, static_cast<int64_t>(H) * s.row_tiles), heads = rows * H * G;
+        // A CTA to an SM and 128 tokens in 1.7 us, or two and 64 tokens in 1.5.
+        const int64_t tile = chunk ? kChunkKeys : 16 * kRowsWarps;
+        s.chunk = static_cast<int32_t>(tile * cut(ceil_div(len, tile), items, longest, heads, D, chunk ? kSms : 2 * kSms,
+                                                  chunk ? 1.7 : 1.5, chunk ? 5 : 4));
+    }
+    s.splits = static_cast<int32_t>(ceil_div(len, s.chunk));
     return s;
 }
 
@@ -152,7 +156,7 @@ kv_join_kernel(const KvRowsArgs g)
 template <int QT>
 int launch_join_t(const KvRowsArgs& g, cudaStream_t stream)
 {
-    if (g.s.splits > 16) return launch_pdl(kv_join_kernel<QT, 16>, static_cast<unsigned>(g.heads), 512, 0, stream, g);
+    if (g.s.splits > 16 && g.heads <= 4096) return launch_pdl(kv_join_kernel<QT, 16>, static_cast<unsigned>(g.heads), 512, 0, stream, g);
     return launch_pdl(kv_join_kernel<QT, 1>, static_cast<unsigned>(ceil_div(g.heads, 8)), 256, 0, stream, g);
 }
 

@@ -191,6 +191,14 @@ __device__ __forceinline__ uint32_t tile_at(int row, int piece)
     return (piece >> 3) * (kChunkKeys * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
+// 32 bytes: a thread's own row, so half as many lines to a warp's stores as with 16.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ void st_shared16(uint32_t at, uint4 x)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
@@ -209,11 +217,10 @@ __device__ __forceinline__ int64_t chunk_off(const KvCache& c, int page, int at,
     return page < 0 ? -1 : kv_off(c, page, h, (at + 16 * lane) & (c.page_tokens - 1));
 }
 
-// The whole 128-token tiles of K and V from `begin` on, in the order K0 V0 K1 V1 ..., into the ring.  Q's copies
-// are on their way already: `q_full` is told when they have come.
+// The whole 128-token tiles of K and V from `begin` on, in the order K0 V0 K1 V1 ..., into the ring.
 template <int D, int FMT>
 __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* table, int table_pages, int h, int begin, int end,
-                                           uint32_t ring, uint32_t full, uint32_t empty, uint32_t q_full)
+                                           uint32_t ring, uint32_t full, uint32_t empty)
 {
     using S = ChunkShape<D, FMT>;
     const int t = threadIdx.x & 127, lane = threadIdx.x & 31;
@@ -250,19 +257,21 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
                     }
                 }
                 asm volatile("cp.async.commit_group;\n" ::: "memory");
-                if (i >= AHEAD) {
+                if (i == 1) {   // the first scores need not wait for what follows
+                    asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+                    fence_async_smem();
+                    mbar_arrive(full);
+                } else if (i > AHEAD) {
                     asm volatile("cp.async.wait_group %0;\n" ::"n"(AHEAD) : "memory");
                     fence_async_smem();
-                    if (i == AHEAD) mbar_arrive(q_full);
                     mbar_arrive(full + 8 * ((i - AHEAD) % S::STAGES));
                 }
             }
         }
         cp_async_wait_all();
         fence_async_smem();
-        if (i <= AHEAD) mbar_arrive(q_full);
         if (ok)
-            for (int k = max(0, i - AHEAD); k < i; ++k) mbar_arrive(full + 8 * (k % S::STAGES));
+            for (int k = max(1, i - AHEAD); k < i; ++k) mbar_arrive(full + 8 * (k % S::STAGES));
     } else {
         // A thread copies 16-code pieces lq, lq + 4 of the rows lr, lr + 32, lr + 64, lr + 96 to a place of its own
         // some tiles ahead, and decodes those same pieces from there.
@@ -310,10 +319,6 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
         int i = 0;
         for (; i < stages && ok; ++i) {
             asm volatile("cp.async.wait_group %0;\n" ::"n"(AHEAD - 1) : "memory");
-            if (i == 0) {
-                fence_async_smem();
-                mbar_arrive(q_full);
-            }
             issue();
             const int st = i % S::STAGES;
             ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((i / S::STAGES) & 1) ^ 1));
@@ -340,10 +345,6 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
             mbar_arrive(full + 8 * st);
         }
         cp_async_wait_all();
-        if (stages == 0) {
-            fence_async_smem();
-            mbar_arrive(q_full);
-        }
     }
     return ok;
 }
@@ -391,7 +392,7 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                 mbar_init(p_full + 16 + 8 * i, 128);   // and the second
                 mbar_init(o_full + 8 * i, 1);
             }
-            mbar_init(q_full, 128);
+            mbar_init(q_full, 256);
             mbar_init(drain, 1);
             asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         }
@@ -472,36 +473,37 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
         __syncwarp();
     } else if (warp >= 8) {
         regs_down<kRegsLoad>();
-        {
-            constexpr int PIECES = D / 8, ROWS = 128 / PIECES;
-            const int t = threadIdx.x & 127, piece = t % PIECES, at_row = t / PIECES;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+        if (!chunk_load<D, FMT>(a.c, table, a.w.table_pages, h, begin, end, ring, full, empty)) atomicOr(fault, kFaultTimeout);
+    } else {
+        regs_up<kRegsSoftmax>();
+        {   // Q, by both row tiles' warps
+            constexpr int PIECES = D / 8, ROWS = 256 / PIECES;
+            const int piece = threadIdx.x % PIECES, at_row = threadIdx.x / PIECES;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(h) * G * a.q_head + piece * 8;
             const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // the softmax uses |scale|
             const bool vec = flip == 0 && ((reinterpret_cast<uintptr_t>(q) & 15) | (a.q_tok & 7) | (a.q_head & 7)) == 0;
+#pragma unroll 4
             for (int row = at_row; row < kChunkRows; row += ROWS) {
-                const int qr = r0 + row;
+                const unsigned qr = min(r0 + row, nrows - 1), tok = qr / static_cast<unsigned>(G), g1 = qr - tok * G;
+                const bool there = r0 + row < nrows;
                 const uint32_t to = q_s + (row >> 7) * S::TILE + tile_at(row & 127, piece);
-                const __nv_bfloat16* from = q;
-                if (qr < nrows)
-                    from += (sp.first + qr / G) * a.q_tok + (static_cast<int64_t>(h) * G + qr % G) * a.q_head + piece * 8;
+                const __nv_bfloat16* from = q + (sp.first + tok) * a.q_tok + g1 * a.q_head;
                 if (vec) {
-                    cp_async16_to(to, from, qr < nrows ? 16 : 0);
+                    cp_async16_to(to, from, there ? 16 : 0);
                 } else {
-                    uint32_t w[4] = {0, 0, 0, 0};
-                    if (qr < nrows) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            w[i] = (__bfloat16_as_ushort(from[2 * i]) |
-                                    static_cast<uint32_t>(__bfloat16_as_ushort(from[2 * i + 1])) << 16) ^ flip;
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = there ? (__bfloat16_as_ushort(from[2 * i]) |
+                                        static_cast<uint32_t>(__bfloat16_as_ushort(from[2 * i + 1])) << 16) ^ flip
+                                     : 0u;
                     st_shared16(to, make_uint4(w[0], w[1], w[2], w[3]));
                 }
             }
-            asm volatile("cp.async.commit_group;\n" ::: "memory");
+            cp_async_wait_all();
+            fence_async_smem();
+            mbar_arrive(q_full);
         }
-        if (!chunk_load<D, FMT>(a.c, table, a.w.table_pages, h, begin, end, ring, full, empty, q_full)) atomicOr(fault, kFaultTimeout);
-    } else {
-        regs_up<kRegsSoftmax>();
         const int t = warp >> 2;
         const int qr = r0 + threadIdx.x;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -604,17 +606,17 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                     for (int k = 0; k < 32; ++k) o[k] = nothing ? 0.0f : o[k] * f;
                     if (qr < nrows) {
                         if (parts) {
-                            float4* to = reinterpret_cast<float4*>(g.po + at_p * D + i);
+                            float* to = g.po + at_p * D + i;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                            for (int k = 0; k < 32; k += 8) st_global32(to + k, reinterpret_cast<const uint32_t*>(o + k));
                         } else {
                             __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + head * D + i;
-                            if ((reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
+                            if ((reinterpret_cast<uintptr_t>(a.out) & 31) == 0) {
+                                uint32_t w[16];
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    reinterpret_cast<uint4*>(to)[k] =
-                                        make_uint4(bf16x2(o[8 * k], o[8 * k + 1]), bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                                   bf16x2(o[8 * k + 4], o[8 * k + 5]), bf16x2(o[8 * k + 6], o[8 * k + 7]));
+                                for (int k = 0; k < 16; ++k) w[k] = bf16x2(o[2 * k], o[2 * k + 1]);
+                                st_global32(to, w);
+                                st_global32(to + 16, w + 8);
                             } else {
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) to[k] = __float2bfloat16(o[k]);
