@@ -84,6 +84,74 @@ __device__ __forceinline__ int kv_sequence(const KvRows& w, int r)
 // the zero codes kept with it into NaN.
 __device__ __forceinline__ float kv_pow2(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// ---- 8-bit codes to bf16, two at a time
+
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t bsub2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// (x & y) | z
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t y, uint32_t z)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+    return r;
+}
+
+// Masks of the decoders, kept in registers: an instruction takes one constant only.
+struct CodeMasks {
+    uint32_t a, b, c;
+};
+
+template <int FMT>
+__device__ __forceinline__ CodeMasks code_masks()
+{
+    CodeMasks m;
+    asm volatile("mov.b32 %0, %3;\n mov.b32 %1, %4;\n mov.b32 %2, %5;\n"
+                 : "=r"(m.a), "=r"(m.b), "=r"(m.c)
+                 : "n"(FMT == FATHOM_KV_INT8 ? 0x007f007f : 0x07f007f0), "n"(FMT == FATHOM_KV_INT8 ? 0x00800080 : 0x80008000),
+                   "n"(0x43004300));
+    return m;
+}
+
+// INT8 codes in the low bytes of each 16 bits as bf16 values, times the powers f:
+// 128 + low 7 bits, less 128, or 256 for a negative code.
+__device__ __forceinline__ uint32_t decode_low(uint32_t t, uint32_t f, const CodeMasks& m)
+{
+    return bmul2(bsub2(and_or(t, m.a, m.c), and_or(t, m.b, m.c)), f);
+}
+
+// E4M3 codes in the high bytes: sign in place, exponent and mantissa 4 below; 2^120 of the power makes up for the bias.
+__device__ __forceinline__ uint32_t decode_high(uint32_t t, uint32_t f, const CodeMasks& m)
+{
+    return bmul2(and_or(t, m.b, (t >> 4) & m.a), f);
+}
+
+// Bytes BLO of x and BHI of y.
+template <int FMT, int BLO, int BHI>
+__device__ __forceinline__ uint32_t decode2(uint32_t x, uint32_t y, uint32_t f, const CodeMasks& m)
+{
+    if (FMT == FATHOM_KV_INT8) return decode_low(__byte_perm(x, y, BLO | ((4 + BHI) << 8)), f, m);
+    return decode_high(__byte_perm(x, y, (BLO << 4) | ((4 + BHI) << 12)), f, m);
+}
+
+// The 16 bits that decode2 multiplies with, from the exponent byte.
+template <int FMT>
+__device__ __forceinline__ uint32_t pow_bits(uint32_t byte)
+{
+    return (FMT == FATHOM_KV_INT8 ? byte : min(byte + 120u, 255u)) << 7;
+}
+
 // Two bf16 from two fp32, the first in the low half.
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 {

@@ -1,14 +1,18 @@
 // fathom_kv_write and fathom_kv_read: rows into the paged cache and back.
 //
-// One thread takes 8 channels of one row of K and of V; the four threads of a
-// 32-channel block find its largest magnitude with two shuffles.  Magnitudes
-// are compared as bit patterns, which orders NaN above infinity above every
-// number, so one compare finds the blocks that cannot be kept.  The exponent
-// comes from the pattern too (exponent field, and one compare of the fraction
-// with the value that would round over the largest code), so no division or
-// logarithm is rounded anywhere and x 2^-e is exact before the one rounding
-// to the code.  Both kernels stream: bound by HBM, or by the launch when a
-// decode step writes one token.
+// A thread takes 16 channels of a few consecutive rows of K and of V; the two
+// threads of a 32-channel block find its largest magnitude with a shuffle.
+// Magnitudes are compared as bit patterns, which orders NaN above infinity
+// above every number, so one compare finds the blocks that cannot be kept.
+// The exponent comes from the pattern too (exponent field, and one compare of
+// the fraction with the value that would round over the largest code), so no
+// division or logarithm is rounded anywhere and x 2^-e is exact before the one
+// rounding to the code.
+//
+// Both kernels stream: bound by HBM, or by the launch when a decode step
+// writes one token.  A row's place is three loads that wait for one another
+// (its sequence, its length, its page): with several rows to a thread their
+// chains and the copies behind them run side by side.
 #include "kv.cuh"
 
 namespace fathom {
@@ -17,50 +21,63 @@ namespace {
 
 constexpr int kKvThreads = 256;
 
-// 8 consecutive elements as fp32.
+// 16 elements as they lie: two 16-byte pieces of bf16, four of fp32.
+template <int DT>
+struct Raw16 {
+    uint4 u[DT == FATHOM_KEYS_BF16 ? 2 : 4];
+};
+
 template <int DT, bool VEC>
-__device__ __forceinline__ void kv_load8(const void* p, int64_t at, float (&x)[8])
+__device__ __forceinline__ void kv_load16(const void* p, int64_t at, Raw16<DT>* raw)
 {
-    if (DT == FATHOM_KEYS_BF16) {
-        const __nv_bfloat16* s = static_cast<const __nv_bfloat16*>(p) + at;
-        if (VEC) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(s));
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    constexpr int N = DT == FATHOM_KEYS_BF16 ? 2 : 4;
+    if (VEC) {
+        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p) + at * (DT == FATHOM_KEYS_BF16 ? 2 : 4));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        } else {
+        for (int i = 0; i < N; ++i) raw->u[i] = __ldg(s + i);
+    } else if (DT == FATHOM_KEYS_BF16) {
+        const unsigned short* s = static_cast<const unsigned short*>(p) + at;
+        uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(s[i]);
-        }
+        for (int i = 0; i < 8; ++i) w[i] = s[2 * i] | static_cast<uint32_t>(s[2 * i + 1]) << 16;
+#pragma unroll
+        for (int i = 0; i < N; ++i) raw->u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     } else {
-        const float* s = static_cast<const float*>(p) + at;
-        if (VEC) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(s)), b = __ldg(reinterpret_cast<const float4*>(s) + 1);
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        } else {
+        const uint32_t* s = static_cast<const uint32_t*>(p) + at;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = s[i];
+        for (int i = 0; i < N; ++i) raw->u[i] = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void kv_values(const Raw16<DT>& raw, float (&x)[16])
+{
+#pragma unroll
+    for (int i = 0; i < (DT == FATHOM_KEYS_BF16 ? 2 : 4); ++i) {
+        const uint32_t w[4] = {raw.u[i].x, raw.u[i].y, raw.u[i].z, raw.u[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (DT == FATHOM_KEYS_BF16) {
+                x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            } else {
+                x[4 * i + j] = __uint_as_float(w[j]);
+            }
         }
     }
 }
 
-// Codes of 8 channels and their block's exponent byte.  All four threads of
-// the block take part.
+// Codes of 16 channels and their block's exponent byte.  Both threads of the block take part.
 template <int FMT>
-__device__ __forceinline__ uint2 kv_encode8(const float (&x)[8], uint32_t* byte)
+__device__ __forceinline__ uint4 kv_encode16(const float (&x)[16], uint32_t* byte)
 {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     if (m >= 0x7f800000u) {
         *byte = 255;
-        return make_uint2(0, 0);
+        return make_uint4(0, 0, 0, 0);
     }
     const int ex = static_cast<int>(m >> 23) - 127;
     const uint32_t frac = m & 0x7fffffu;
@@ -69,39 +86,46 @@ __device__ __forceinline__ uint2 kv_encode8(const float (&x)[8], uint32_t* byte)
     e = min(max(e, kKvLowest), FMT == FATHOM_KV_INT8 ? 121 : 7);
     *byte = static_cast<uint32_t>(e + 127);
     const float f = kv_pow2(static_cast<uint32_t>(127 - e));
-    uint32_t w[2];
+    uint32_t w[4];
+    const float most = FMT == FATHOM_KV_INT8 && e == 121 ? 127.0f / f : INFINITY;   // only there a code could become 128
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
         if (FMT == FATHOM_KV_INT8) {
-            w[i] = 0;
+            // x f + 1.5 2^23: the product is exact, the sum is rounded to a whole number, kept in its low bits
+            uint32_t r[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = min(127, max(-127, __float2int_rn(x[4 * i + j] * f)));
-                w[i] |= static_cast<uint32_t>(c & 0xff) << (8 * j);
-            }
+            for (int j = 0; j < 4; ++j)
+                r[j] = __float_as_uint(fmaf(fminf(fmaxf(x[4 * i + j], -most), most), f, 12582912.0f));
+            w[i] = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
         } else {
             const float2 lo = make_float2(x[4 * i] * f, x[4 * i + 1] * f), hi = make_float2(x[4 * i + 2] * f, x[4 * i + 3] * f);
             w[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3)) |
                    static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3)) << 16;
         }
     }
-    return make_uint2(w[0], w[1]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Values of 8 codes (exact: at most 7 bits times a power of two).
+// Values of 16 codes as bf16 pairs (exact: at most 7 bits times a power of two).
 template <int FMT>
-__device__ __forceinline__ void kv_decode8(uint2 c, uint32_t byte, float (&x)[8])
+__device__ __forceinline__ void kv_decode16(uint4 c, uint32_t byte, uint32_t (&x)[8])
 {
-    const float f = kv_pow2(byte);
-    const uint32_t w[2] = {c.x, c.y};
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    if constexpr (FMT == FATHOM_KV_INT8) {
+        const CodeMasks m = code_masks<FMT>();
+        const uint32_t f = pow_bits<FMT>(byte) * 0x10001u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t b = (w[i >> 2] >> (8 * (i & 3))) & 0xff;
-        if (FMT == FATHOM_KV_INT8) {
-            x[i] = static_cast<float>(static_cast<int8_t>(b)) * f;
-        } else {
-            const __half_raw r = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3);
-            x[i] = __half2float(__half(r)) * f;
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = decode2<FMT, 0, 1>(w[i], w[i], f, m);
+            x[2 * i + 1] = decode2<FMT, 2, 3>(w[i], w[i], f, m);
+        }
+    } else {
+        const float f = kv_pow2(byte);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+            const float2 v = __half22float2(__half2(r));
+            x[i] = bf16x2(v.x * f, v.y * f);
         }
     }
 }
@@ -116,46 +140,87 @@ __device__ __forceinline__ int kv_place(const KvCache& c, const KvRows& w, int r
     return kv_page(c, w.table + b * w.table_stride, w.table_pages, pos);
 }
 
+// Rows of a thread.
+template <int DT>
+__host__ __device__ constexpr int kv_rows_each() { return DT == FATHOM_KEYS_BF16 ? 4 : 2; }
+
 template <int FMT, int DT, bool VEC>
 __global__ void __launch_bounds__(kKvThreads)
 kv_write_kernel(const KvCache c, const KvRows w, const void* __restrict__ k, const void* __restrict__ v,
                 int64_t stride_tok, int64_t stride_h)
 {
-    const int per = c.D >> 3;
+    constexpr int N = kv_rows_each<DT>();
+    const int per = c.D >> 4, units = c.H * per;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x;
-    const int64_t unit = t / per;
-    const int j = static_cast<int>(t - unit * per) << 3;
-    const int64_t row = unit / c.H;
-    const int h = static_cast<int>(unit - row * c.H);
-    int page = -2, token = 0;
-    if (row < w.rows) page = kv_place(c, w, static_cast<int>(row), &token);
-    const bool live = page >= 0;   // the same for the four threads of a block
-    float x[2][8];
-    const int64_t at = live ? row * stride_tok + h * stride_h + j : 0;
-    if (live) {
-        kv_load8<DT, VEC>(k, at, x[0]);
-        kv_load8<DT, VEC>(v, at, x[1]);
-    } else {
+    const int64_t first = t / units;
+    const int unit = static_cast<int>(t - first * units), h = unit / per, j = (unit - h * per) << 4;
+    int page[N], token[N];
+    Raw16<DT> x[N][2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[0][i] = x[1][i] = 0.0f;
+    for (int i = 0; i < N; ++i) {
+        const int64_t row = first * N + i;
+        page[i] = row < w.rows ? kv_place(c, w, static_cast<int>(row), &token[i]) : -2;
+        x[i][0] = x[i][1] = {};
+        if (page[i] >= 0) {   // the same for both threads of a block
+            const int64_t at = row * stride_tok + h * stride_h + j;
+            kv_load16<DT, VEC>(k, at, &x[i][0]);
+            kv_load16<DT, VEC>(v, at, &x[i][1]);
+        }
     }
-    const int64_t to = live ? kv_off(c, page, h, token) : 0;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        unsigned char* data = const_cast<unsigned char*>(s ? c.v : c.k);
-        if (FMT == FATHOM_KV_BF16) {
-            if (live)
-                *reinterpret_cast<uint4*>(data + to + 2 * j) =
-                    make_uint4(bf16x2(x[s][0], x[s][1]), bf16x2(x[s][2], x[s][3]), bf16x2(x[s][4], x[s][5]),
-                               bf16x2(x[s][6], x[s][7]));
-        } else {
-            uint32_t byte;
-            const uint2 codes = kv_encode8<FMT>(x[s], &byte);
-            if (live) {
-                *reinterpret_cast<uint2*>(data + to + j) = codes;
-                unsigned char* sc = const_cast<unsigned char*>(s ? c.vs : c.ks);
-                if ((j & 31) == 0) sc[kv_scale_off(c, page, h, token) + (j >> 5)] = static_cast<unsigned char>(byte);
+    for (int i = 0; i < N; ++i) {
+        const bool live = page[i] >= 0;
+        const int64_t to = live ? kv_off(c, page[i], h, token[i]) : 0;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            unsigned char* data = const_cast<unsigned char*>(s ? c.v : c.k);
+            float y[16];
+            kv_values<DT>(x[i][s], y);
+            if (FMT == FATHOM_KV_BF16) {
+                if (live) {
+                    uint4* o = reinterpret_cast<uint4*>(data + to + 2 * j);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        o[q] = make_uint4(bf16x2(y[8 * q], y[8 * q + 1]), bf16x2(y[8 * q + 2], y[8 * q + 3]),
+                                          bf16x2(y[8 * q + 4], y[8 * q + 5]), bf16x2(y[8 * q + 6], y[8 * q + 7]));
+                }
+            } else {
+                uint32_t byte;
+                const uint4 codes = kv_encode16<FMT>(y, &byte);
+                if (live) {
+                    *reinterpret_cast<uint4*>(data + to + j) = codes;
+                    unsigned char* sc = const_cast<unsigned char*>(s ? c.vs : c.ks);
+                    if ((j & 31) == 0) sc[kv_scale_off(c, page[i], h, token[i]) + (j >> 5)] = static_cast<unsigned char>(byte);
+                }
             }
+        }
+    }
+}
+
+// 16 values, given as bf16 pairs.
+template <int DT, bool VEC>
+__device__ __forceinline__ void kv_store16(void* out, int64_t to, const uint32_t (&x)[8])
+{
+    if (DT == FATHOM_KEYS_BF16) {
+        unsigned short* o = static_cast<unsigned short*>(out) + to;
+        if (VEC) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                reinterpret_cast<uint4*>(o)[q] = make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = static_cast<unsigned short>(x[i >> 1] >> (16 * (i & 1)));
+        }
+    } else {
+        uint32_t* o = static_cast<uint32_t*>(out) + to;
+        if (VEC) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                reinterpret_cast<uint4*>(o)[q] = make_uint4(x[2 * q] << 16, x[2 * q] & 0xffff0000u, x[2 * q + 1] << 16,
+                                                            x[2 * q + 1] & 0xffff0000u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = (i & 1) ? x[i >> 1] & 0xffff0000u : x[i >> 1] << 16;
         }
     }
 }
@@ -164,50 +229,54 @@ template <int FMT, int DT, bool VEC>
 __global__ void __launch_bounds__(kKvThreads)
 kv_read_kernel(const KvCache c, const KvRows w, void* out_k, void* out_v, int64_t stride_h, int64_t stride_tok)
 {
-    const int per = c.D >> 3;
+    constexpr int N = kv_rows_each<DT>(), PIECES = FMT == FATHOM_KV_BF16 ? 2 : 1;
+    const int per = c.D >> 4;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x;
-    const int64_t row = t / per;
-    const int j = static_cast<int>(t - row * per) << 3;
+    const int64_t first = t / per;
+    const int j = static_cast<int>(t - first * per) << 4;
     const int h = blockIdx.y;
-    if (row >= w.rows) return;
-    int token = 0;
-    const int page = kv_place(c, w, static_cast<int>(row), &token);
-    if (page == -2) return;   // not a row of any sequence
-    const int64_t from = page >= 0 ? kv_off(c, page, h, token) : 0;
-    const int64_t to = h * stride_h + row * stride_tok + j;
+    int page[N], token[N];
+    uint4 raw[N][2][PIECES];
+    uint32_t byte[N][2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        void* out = s ? out_v : out_k;
-        if (!out) continue;
-        const unsigned char* data = s ? c.v : c.k;
-        float x[8] = {};
-        if (page >= 0) {
-            if (FMT == FATHOM_KV_BF16) {
-                kv_load8<FATHOM_KEYS_BF16, true>(data + from, j, x);
-            } else {
-                const uint2 codes = __ldg(reinterpret_cast<const uint2*>(data + from + j));
-                const uint32_t byte = __ldg((s ? c.vs : c.ks) + kv_scale_off(c, page, h, token) + (j >> 5));
-                kv_decode8<FMT>(codes, byte, x);
+    for (int i = 0; i < N; ++i) {
+        const int64_t row = first * N + i;
+        page[i] = row < w.rows ? kv_place(c, w, static_cast<int>(row), &token[i]) : -2;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            byte[i][s] = 0;
+#pragma unroll
+            for (int q = 0; q < PIECES; ++q) raw[i][s][q] = make_uint4(0, 0, 0, 0);
+            if (page[i] >= 0 && (s ? out_v : out_k)) {
+                const uint4* from = reinterpret_cast<const uint4*>((s ? c.v : c.k) + kv_off(c, page[i], h, token[i]) + j * kv_elem_bytes<FMT>());
+#pragma unroll
+                for (int q = 0; q < PIECES; ++q) raw[i][s][q] = __ldg(from + q);
+                if (FMT != FATHOM_KV_BF16)
+                    byte[i][s] = __ldg((s ? c.vs : c.ks) + kv_scale_off(c, page[i], h, token[i]) + (j >> 5));
             }
         }
-        if (DT == FATHOM_KEYS_BF16) {
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + to;
-            const uint4 u = make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
-            if (VEC) {
-                *reinterpret_cast<uint4*>(o) = u;
-            } else {
+    }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __float2bfloat16(x[i]);
-            }
-        } else {
-            float* o = static_cast<float*>(out) + to;
-            if (VEC) {
-                reinterpret_cast<float4*>(o)[0] = make_float4(x[0], x[1], x[2], x[3]);
-                reinterpret_cast<float4*>(o)[1] = make_float4(x[4], x[5], x[6], x[7]);
-            } else {
+    for (int i = 0; i < N; ++i) {
+        if (page[i] == -2) continue;   // not a row of any sequence
+        const int64_t to = h * stride_h + (first * N + i) * stride_tok + j;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = x[i];
+        for (int s = 0; s < 2; ++s) {
+            void* out = s ? out_v : out_k;
+            if (!out) continue;
+            uint32_t x[8];
+            if constexpr (FMT == FATHOM_KV_BF16) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    x[4 * q] = raw[i][s][q].x;
+                    x[4 * q + 1] = raw[i][s][q].y;
+                    x[4 * q + 2] = raw[i][s][q].z;
+                    x[4 * q + 3] = raw[i][s][q].w;
+                }
+            } else {
+                kv_decode16<FMT>(raw[i][s][0], byte[i][s], x);
             }
+            kv_store16<DT, VEC>(out, to, x);
         }
     }
 }
@@ -216,8 +285,8 @@ template <int FMT>
 int launch_kv_write_f(const KvCache& c, const KvRows& w, const void* k, const void* v, int dtype, bool vec,
                       int64_t stride_tok, int64_t stride_h, cudaStream_t stream)
 {
-    const int64_t threads = static_cast<int64_t>(w.rows) * c.H * (c.D / 8);
-    const unsigned grid = static_cast<unsigned>(ceil_div(threads, kKvThreads));
+    const int64_t each = dtype == FATHOM_KEYS_BF16 ? kv_rows_each<FATHOM_KEYS_BF16>() : kv_rows_each<FATHOM_KEYS_F32>();
+    const unsigned grid = static_cast<unsigned>(ceil_div(ceil_div(w.rows, each) * c.H * (c.D / 16), kKvThreads));
     if (dtype == FATHOM_KEYS_BF16) {
         if (vec) kv_write_kernel<FMT, FATHOM_KEYS_BF16, true><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
         else kv_write_kernel<FMT, FATHOM_KEYS_BF16, false><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
@@ -232,8 +301,8 @@ template <int FMT>
 int launch_kv_read_f(const KvCache& c, const KvRows& w, void* out_k, void* out_v, int dtype, bool vec,
                      int64_t stride_h, int64_t stride_tok, cudaStream_t stream)
 {
-    const int64_t threads = static_cast<int64_t>(w.rows) * (c.D / 8);
-    const dim3 grid(static_cast<unsigned>(ceil_div(threads, kKvThreads)), static_cast<unsigned>(c.H));
+    const int64_t each = dtype == FATHOM_KEYS_BF16 ? kv_rows_each<FATHOM_KEYS_BF16>() : kv_rows_each<FATHOM_KEYS_F32>();
+    const dim3 grid(static_cast<unsigned>(ceil_div(ceil_div(w.rows, each) * (c.D / 16), kKvThreads)), static_cast<unsigned>(c.H));
     if (dtype == FATHOM_KEYS_BF16) {
         if (vec) kv_read_kernel<FMT, FATHOM_KEYS_BF16, true><<<grid, kKvThreads, 0, stream>>>(c, w, out_k, out_v, stride_h, stride_tok);
         else kv_read_kernel<FMT, FATHOM_KEYS_BF16, false><<<grid, kKvThreads, 0, stream>>>(c, w, out_k, out_v, stride_h, stride_tok);
@@ -244,7 +313,7 @@ int launch_kv_read_f(const KvCache& c, const KvRows& w, void* out_k, void* out_v
     return launch_status();
 }
 
-// 16-byte pieces: 8 elements of `dtype` start on a multiple of 16 bytes everywhere.
+// 16-byte pieces: 16 elements of `dtype` start on a multiple of 16 bytes everywhere.
 bool kv_vec(const void* a, const void* b, int dtype, int64_t s0, int64_t s1)
 {
     const int64_t esz = dtype == FATHOM_KEYS_F32 ? 4 : 2;
