@@ -152,6 +152,14 @@ __device__ __forceinline__ uint32_t pow_bits(uint32_t byte)
     return (FMT == FATHOM_KV_INT8 ? byte : min(byte + 120u, 255u)) << 7;
 }
 
+// 32 bytes at once: half as many lines to a warp's stores as with 16, where each thread has its own.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // Two bf16 from two fp32, the first in the low half.
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 {

@@ -20,6 +20,14 @@ namespace fathom {
 namespace {
 
 constexpr int kKvThreads = 256;
+constexpr int64_t kKvOneEach = 148 * 1024;   // threads that are one wave
+
+__device__ __forceinline__ void ld_global32(const void* p, uint4* u)
+{
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(u[0].x), "=r"(u[0].y), "=r"(u[0].z), "=r"(u[0].w), "=r"(u[1].x), "=r"(u[1].y), "=r"(u[1].z), "=r"(u[1].w)
+                 : "l"(p));
+}
 
 // 16 elements as they lie: two 16-byte pieces of bf16, four of fp32.
 template <int DT>
@@ -27,14 +35,22 @@ struct Raw16 {
     uint4 u[DT == FATHOM_KEYS_BF16 ? 2 : 4];
 };
 
-template <int DT, bool VEC>
+// VEC: bytes that all pieces are aligned to (32, 16, or 0 for less).  Whole sectors with one instruction where that is 32.
+template <int DT, int VEC>
 __device__ __forceinline__ void kv_load16(const void* p, int64_t at, Raw16<DT>* raw)
 {
     constexpr int N = DT == FATHOM_KEYS_BF16 ? 2 : 4;
     if (VEC) {
         const uint4* s = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p) + at * (DT == FATHOM_KEYS_BF16 ? 2 : 4));
 #pragma unroll
-        for (int i = 0; i < N; ++i) raw->u[i] = __ldg(s + i);
+        for (int i = 0; i < N; i += 2) {
+            if (VEC == 32) {
+                ld_global32(s + i, &raw->u[i]);
+            } else {
+                raw->u[i] = __ldg(s + i);
+                raw->u[i + 1] = __ldg(s + i + 1);
+            }
+        }
     } else if (DT == FATHOM_KEYS_BF16) {
         const unsigned short* s = static_cast<const unsigned short*>(p) + at;
         uint32_t w[8];
@@ -140,16 +156,11 @@ __device__ __forceinline__ int kv_place(const KvCache& c, const KvRows& w, int r
     return kv_page(c, w.table + b * w.table_stride, w.table_pages, pos);
 }
 
-// Rows of a thread.
-template <int DT>
-__host__ __device__ constexpr int kv_rows_each() { return DT == FATHOM_KEYS_BF16 ? 4 : 2; }
-
-template <int FMT, int DT, bool VEC>
+template <int FMT, int DT, int VEC, int N>
 __global__ void __launch_bounds__(kKvThreads)
 kv_write_kernel(const KvCache c, const KvRows w, const void* __restrict__ k, const void* __restrict__ v,
                 int64_t stride_tok, int64_t stride_h)
 {
-    constexpr int N = kv_rows_each<DT>();
     const int per = c.D >> 4, units = c.H * per;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x;
     const int64_t first = t / units;
@@ -198,12 +209,14 @@ kv_write_kernel(const KvCache c, const KvRows w, const void* __restrict__ k, con
 }
 
 // 16 values, given as bf16 pairs.
-template <int DT, bool VEC>
+template <int DT, int VEC>
 __device__ __forceinline__ void kv_store16(void* out, int64_t to, const uint32_t (&x)[8])
 {
     if (DT == FATHOM_KEYS_BF16) {
         unsigned short* o = static_cast<unsigned short*>(out) + to;
-        if (VEC) {
+        if (VEC == 32) {
+            st_global32(o, x);
+        } else if (VEC) {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
                 reinterpret_cast<uint4*>(o)[q] = make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
@@ -213,7 +226,15 @@ __device__ __forceinline__ void kv_store16(void* out, int64_t to, const uint32_t
         }
     } else {
         uint32_t* o = static_cast<uint32_t*>(out) + to;
-        if (VEC) {
+        if (VEC == 32) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = (i & 1) ? x[4 * q + (i >> 1)] & 0xffff0000u : x[4 * q + (i >> 1)] << 16;
+                st_global32(o + 8 * q, y);
+            }
+        } else if (VEC) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 reinterpret_cast<uint4*>(o)[q] = make_uint4(x[2 * q] << 16, x[2 * q] & 0xffff0000u, x[2 * q + 1] << 16,
@@ -225,11 +246,11 @@ __device__ __forceinline__ void kv_store16(void* out, int64_t to, const uint32_t
     }
 }
 
-template <int FMT, int DT, bool VEC>
+template <int FMT, int DT, int VEC, int N>
 __global__ void __launch_bounds__(kKvThreads)
 kv_read_kernel(const KvCache c, const KvRows w, void* out_k, void* out_v, int64_t stride_h, int64_t stride_tok)
 {
-    constexpr int N = kv_rows_each<DT>(), PIECES = FMT == FATHOM_KV_BF16 ? 2 : 1;
+    constexpr int PIECES = FMT == FATHOM_KV_BF16 ? 2 : 1;
     const int per = c.D >> 4;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x;
     const int64_t first = t / per;
@@ -281,44 +302,73 @@ kv_read_kernel(const KvCache c, const KvRows w, void* out_k, void* out_v, int64_
     }
 }
 
-template <int FMT>
-int launch_kv_write_f(const KvCache& c, const KvRows& w, const void* k, const void* v, int dtype, bool vec,
-                      int64_t stride_tok, int64_t stride_h, cudaStream_t stream)
+// One row to a thread while that is a wave of threads at most (a token or a few: the chain of loads is the time);
+// beyond, four of bf16 or two of fp32.
+template <int FMT, int DT, int VEC>
+int launch_kv_write_v(const KvCache& c, const KvRows& w, const void* k, const void* v, int64_t stride_tok, int64_t stride_h,
+                      cudaStream_t stream)
 {
-    const int64_t each = dtype == FATHOM_KEYS_BF16 ? kv_rows_each<FATHOM_KEYS_BF16>() : kv_rows_each<FATHOM_KEYS_F32>();
-    const unsigned grid = static_cast<unsigned>(ceil_div(ceil_div(w.rows, each) * c.H * (c.D / 16), kKvThreads));
-    if (dtype == FATHOM_KEYS_BF16) {
-        if (vec) kv_write_kernel<FMT, FATHOM_KEYS_BF16, true><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
-        else kv_write_kernel<FMT, FATHOM_KEYS_BF16, false><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
+    constexpr int N = DT == FATHOM_KEYS_BF16 ? 4 : 2;
+    const int64_t units = static_cast<int64_t>(c.H) * (c.D / 16);
+    if (w.rows * units <= kKvOneEach) {
+        const unsigned grid = static_cast<unsigned>(ceil_div(w.rows * units, kKvThreads));
+        kv_write_kernel<FMT, DT, VEC, 1><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
     } else {
-        if (vec) kv_write_kernel<FMT, FATHOM_KEYS_F32, true><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
-        else kv_write_kernel<FMT, FATHOM_KEYS_F32, false><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
+        const unsigned grid = static_cast<unsigned>(ceil_div(ceil_div(w.rows, N) * units, kKvThreads));
+        kv_write_kernel<FMT, DT, VEC, N><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
+    }
+    return launch_status();
+}
+
+template <int FMT, int DT, int VEC>
+int launch_kv_read_v(const KvCache& c, const KvRows& w, void* out_k, void* out_v, int64_t stride_h, int64_t stride_tok,
+                     cudaStream_t stream)
+{
+    constexpr int N = DT == FATHOM_KEYS_BF16 ? 4 : 2;
+    const int64_t per = c.D / 16;
+    if (w.rows * per * c.H <= kKvOneEach) {
+        const dim3 grid(static_cast<unsigned>(ceil_div(w.rows * per, kKvThreads)), static_cast<unsigned>(c.H));
+        kv_read_kernel<FMT, DT, VEC, 1><<<grid, kKvThreads, 0, stream>>>(c, w, out_k, out_v, stride_h, stride_tok);
+    } else {
+        const dim3 grid(static_cast<unsigned>(ceil_div(ceil_div(w.rows, N) * per, kKvThreads)), static_cast<unsigned>(c.H));
+        kv_read_kernel<FMT, DT, VEC, N><<<grid, kKvThreads, 0, stream>>>(c, w, out_k, out_v, stride_h, stride_tok);
     }
     return launch_status();
 }
 
 template <int FMT>
-int launch_kv_read_f(const KvCache& c, const KvRows& w, void* out_k, void* out_v, int dtype, bool vec,
-                     int64_t stride_h, int64_t stride_tok, cudaStream_t stream)
+int launch_kv_write_f(const KvCache& c, const KvRows& w, const void* k, const void* v, int dtype, int vec, int64_t st, int64_t sh,
+                      cudaStream_t stream)
 {
-    const int64_t each = dtype == FATHOM_KEYS_BF16 ? kv_rows_each<FATHOM_KEYS_BF16>() : kv_rows_each<FATHOM_KEYS_F32>();
-    const dim3 grid(static_cast<unsigned>(ceil_div(ceil_div(w.rows, each) * (c.D / 16), kKvThreads)), static_cast<unsigned>(c.H));
-    if (dtype == FATHOM_KEYS_BF16) {
-        if (vec) kv_read_kernel<FMT, FATHOM_KEYS_BF16, true><<<grid, kKvThreads, 0, stream>>>(c, w, out_k, out_v, stride_h, stride_tok);
-        else kv_read_kernel<FMT, FATHOM_KEYS_BF16, false><<<grid, kKvThreads, 0, stream>>>(c, w, out_k, out_v, stride_h, stride_tok);
-    } else {
-        if (vec) kv_read_kernel<FMT, FATHOM_KEYS_F32, true><<<grid, kKvThreads, 0, stream>>>(c, w, out_k, out_v, stride_h, stride_tok);
-        else kv_read_kernel<FMT, FATHOM_KEYS_F32, false><<<grid, kKvThreads, 0, stream>>>(c, w, out_k, out_v, stride_h, stride_tok);
-    }
-    return launch_status();
+    if (dtype == FATHOM_KEYS_BF16)
+        return vec == 32 ? launch_kv_write_v<FMT, FATHOM_KEYS_BF16, 32>(c, w, k, v, st, sh, stream)
+               : vec     ? launch_kv_write_v<FMT, FATHOM_KEYS_BF16, 16>(c, w, k, v, st, sh, stream)
+                         : launch_kv_write_v<FMT, FATHOM_KEYS_BF16, 0>(c, w, k, v, st, sh, stream);
+    return vec == 32 ? launch_kv_write_v<FMT, FATHOM_KEYS_F32, 32>(c, w, k, v, st, sh, stream)
+           : vec     ? launch_kv_write_v<FMT, FATHOM_KEYS_F32, 16>(c, w, k, v, st, sh, stream)
+                     : launch_kv_write_v<FMT, FATHOM_KEYS_F32, 0>(c, w, k, v, st, sh, stream);
 }
 
-// 16-byte pieces: 16 elements of `dtype` start on a multiple of 16 bytes everywhere.
-bool kv_vec(const void* a, const void* b, int dtype, int64_t s0, int64_t s1)
+template <int FMT>
+int launch_kv_read_f(const KvCache& c, const KvRows& w, void* k, void* v, int dtype, int vec, int64_t sh, int64_t st,
+                     cudaStream_t stream)
+{
+    if (dtype == FATHOM_KEYS_BF16)
+        return vec == 32 ? launch_kv_read_v<FMT, FATHOM_KEYS_BF16, 32>(c, w, k, v, sh, st, stream)
+               : vec     ? launch_kv_read_v<FMT, FATHOM_KEYS_BF16, 16>(c, w, k, v, sh, st, stream)
+                         : launch_kv_read_v<FMT, FATHOM_KEYS_BF16, 0>(c, w, k, v, sh, st, stream);
+    return vec == 32 ? launch_kv_read_v<FMT, FATHOM_KEYS_F32, 32>(c, w, k, v, sh, st, stream)
+           : vec     ? launch_kv_read_v<FMT, FATHOM_KEYS_F32, 16>(c, w, k, v, sh, st, stream)
+                     : launch_kv_read_v<FMT, FATHOM_KEYS_F32, 0>(c, w, k, v, sh, st, stream);
+}
+
+// Bytes that every 16 elements of `dtype` are aligned to: 32, 16, or 0 for less.
+int kv_vec(const void* a, const void* b, int dtype, int64_t s0, int64_t s1)
 {
     const int64_t esz = dtype == FATHOM_KEYS_F32 ? 4 : 2;
-    const uintptr_t p = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b);   // NULL adds no bits
-    return (p & 15) == 0 && (s0 * esz) % 16 == 0 && (s1 * esz) % 16 == 0;
+    const uintptr_t all = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |   // NULL adds no bits
+                          static_cast<uintptr_t>(s0 * esz) | static_cast<uintptr_t>(s1 * esz);
+    return (all & 31) == 0 ? 32 : (all & 15) == 0 ? 16 : 0;
 }
 
 }  // namespace
@@ -326,7 +376,7 @@ bool kv_vec(const void* a, const void* b, int dtype, int64_t s0, int64_t s1)
 int launch_kv_write(const KvCache& c, int format, const KvRows& w, const void* k, const void* v, int dtype,
                     int64_t stride_tok, int64_t stride_h, cudaStream_t stream)
 {
-    const bool vec = kv_vec(k, v, dtype, stride_tok, stride_h);
+    const int vec = kv_vec(k, v, dtype, stride_tok, stride_h);
     switch (format) {
         case FATHOM_KV_BF16: return launch_kv_write_f<FATHOM_KV_BF16>(c, w, k, v, dtype, vec, stride_tok, stride_h, stream);
         case FATHOM_KV_INT8: return launch_kv_write_f<FATHOM_KV_INT8>(c, w, k, v, dtype, vec, stride_tok, stride_h, stream);
@@ -337,7 +387,7 @@ int launch_kv_write(const KvCache& c, int format, const KvRows& w, const void* k
 int launch_kv_read(const KvCache& c, int format, const KvRows& w, void* out_k, void* out_v, int dtype,
                    int64_t stride_h, int64_t stride_tok, cudaStream_t stream)
 {
-    const bool vec = kv_vec(out_k, out_v, dtype, stride_h, stride_tok);
+    const int vec = kv_vec(out_k, out_v, dtype, stride_h, stride_tok);
     switch (format) {
         case FATHOM_KV_BF16: return launch_kv_read_f<FATHOM_KV_BF16>(c, w, out_k, out_v, dtype, vec, stride_h, stride_tok, stream);
         case FATHOM_KV_INT8: return launch_kv_read_f<FATHOM_KV_INT8>(c, w, out_k, out_v, dtype, vec, stride_h, stride_tok, stream);

@@ -191,14 +191,6 @@ __device__ __forceinline__ uint32_t tile_at(int row, int piece)
     return (piece >> 3) * (kChunkKeys * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
-// 32 bytes: a thread's own row, so half as many lines to a warp's stores as with 16.
-__device__ __forceinline__ void st_global32(void* p, const uint32_t* w)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
 __device__ __forceinline__ void st_shared16(uint32_t at, uint4 x)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
