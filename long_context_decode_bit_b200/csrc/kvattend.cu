@@ -46,7 +46,7 @@ KvSplit rows_split(int H, int G, int D, int64_t rows, int B, int64_t max_new, in
     if (s.nt == 1) {
         // Single tokens.  Four CTAs fit an SM.  One session: its stretches are equal, one wave of CTAs.  Several of
         // uneven lengths: shorter stretches, so that the longest session does not end alone.
-        const int64_t items = static_cast<int64_t>(B) * H, want = B == 1 ? 4 * kSms : 32 * kSms;
+        const int64_t items = static_cast<int64_t>(B) * H, want = B == 1 ? 4 * kSms : 16 * kSms;
         const int64_t splits = std::max<int64_t>(1, want / items);
         s.chunk = static_cast<int32_t>(std::max<int64_t>(round_up(ceil_div(len, splits), 64), 256));
     } else {
@@ -62,11 +62,15 @@ KvSplit rows_split(int H, int G, int D, int64_t rows, int B, int64_t max_new, in
     return s;
 }
 
+// A union has between 1/G of M rows and all of them, only the device knows:
+// 5/8 is taken, and one wave of CTAs, four to an SM, for that (a group's last
+// stretch is half one on average).
 KvSplit union_split(int64_t H, int64_t M)
 {
     KvSplit s{1, 8, 1, 1, 0};
-    const int64_t splits = std::max<int64_t>(1, 4 * kSms / H);
-    s.chunk = static_cast<int32_t>(std::max<int64_t>(round_up(ceil_div(M, splits), 64), 64));
+    const double per_group = 4.0 * kSms / static_cast<double>(H) - 0.5;
+    const int64_t chunk = per_group > 0.625 ? static_cast<int64_t>(0.625 * static_cast<double>(M) / per_group) : M;
+    s.chunk = static_cast<int32_t>(round_up(std::max<int64_t>(std::min(chunk, M), 1), 64));
     s.splits = static_cast<int32_t>(ceil_div(M, s.chunk));
     return s;
 }
@@ -88,25 +92,29 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS)
 kv_join_kernel(const KvRowsArgs g)
 {
     constexpr int HEADS = WARPS == 1 ? 8 : 1;   // of a CTA
-    pdl_wait();
     const KvAttend& a = g.a;
     const int D = a.c.D, lane = threadIdx.x & 31, heads_row = a.c.H * a.G;
     const int warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
     const int64_t head = static_cast<int64_t>(blockIdx.x) * HEADS + (WARPS == 1 ? threadIdx.x >> 5 : 0);
-    if (head >= g.heads) return;
-    const int row = static_cast<int>(head / heads_row), hq = static_cast<int>(head - static_cast<int64_t>(row) * heads_row);
-    int n;   // stretches that were computed
-    if (a.uni) {
-        n = static_cast<int>(ceil_div(min(static_cast<int64_t>(max(a.count[hq / a.G], 0)), a.M), g.s.chunk));
+    int n = 0;   // stretches that were computed; -1: the row is not
+    if (head >= g.heads) {
+        n = -1;
+    } else if (a.uni) {
+        n = static_cast<int>(ceil_div(min(static_cast<int64_t>(max(a.count[head / a.G], 0)), a.M), g.s.chunk));
     } else {
-        const int b = kv_sequence(a.w, row);
-        if (b < 0) return;
-        const KvSpan sp = kv_span(a, b);
-        if (row - sp.first >= sp.rows) return;
-        const int qr = static_cast<int>(row - sp.first) * a.G + hq % a.G;
-        const int r0 = qr / g.s.tile_rows * g.s.tile_rows;
-        n = static_cast<int>(ceil_div(kv_tile_keys(a, sp, r0, g.s.tile_rows), g.s.chunk));
+        const int row = static_cast<int>(head / heads_row), b = kv_sequence(a.w, row);
+        const KvSpan sp = kv_span(a, max(b, 0));
+        if (b < 0 || row - sp.first >= sp.rows) {
+            n = -1;
+        } else {
+            const int qr = static_cast<int>(row - sp.first) * a.G + static_cast<int>(head % heads_row) % a.G;
+            n = static_cast<int>(ceil_div(kv_tile_keys(a, sp, qr / g.s.tile_rows * g.s.tile_rows, g.s.tile_rows), g.s.chunk));
+        }
     }
+    // The lengths are the caller's; the parts are written by the kernel before.  Every CTA waits: the stream's next
+    // kernel starts when this one has ended, and counts on both.
+    pdl_wait();
+    if (n < 0) return;
     float top = -INFINITY;
     for (int s = lane; s < n; s += 32) top = fmaxf(top, g.pm[s * g.heads + head]);
 #pragma unroll

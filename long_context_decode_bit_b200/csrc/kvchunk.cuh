@@ -354,6 +354,7 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                    q_full = o_full + 16, drain = q_full + 8, tmem_slot = drain + 8;
     static_assert(16 * ST + 16 * 4 + 8 * 2 + 4 <= 256, "barriers fit their space");
 
+    pdl_launch_dependents();   // kv_join_kernel gets ready meanwhile
     const KvAttend& a = g.a;
     // the same in all lanes, as the compiler can tell
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -629,7 +630,6 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
         tc_after();
         tmem_free(tmem, 512);
     }
-    pdl_launch_dependents();
 }
 
 template <int D, int FMT>

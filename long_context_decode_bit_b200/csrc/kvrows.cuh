@@ -190,8 +190,8 @@ struct RowsShape {
     static constexpr int QB = static_cast<int>(sizeof(uint2)) * NQ * KS * NT * 32; // Q's operand registers
     static constexpr int OB = static_cast<int>(sizeof(float)) * NT * 8 * (D + 8);  // value sums, where the ring was
     static constexpr int SUMS = QB + (RING > OB ? RING : OB);
-    static constexpr int SMEM = SUMS + static_cast<int>(sizeof(float)) * NT * 8 * 2 * kRowsWarps;
-    static constexpr int FIT = 225 * 1024 / (SMEM + 1024);
+    static constexpr int SMEM = SUMS + static_cast<int>(sizeof(float)) * NT * 8 * (2 * kRowsWarps + 2);
+    static constexpr int FIT = 228 * 1024 / (SMEM + 1024);
     static constexpr int CTAS = NT == 1 && D <= 128 ? (FIT < 4 ? FIT : 4) : (FIT < 2 ? FIT : 2);   // to an SM
 
     // 16-byte piece of a row in its tile: moved so that the lanes that read together find different banks.
@@ -225,6 +225,7 @@ kv_rows_kernel(const KvRowsArgs g)
     float* os = reinterpret_cast<float*>(smem + S::QB);               // [NT*8][D+8] value sums, after the loop
     float* sm_m = reinterpret_cast<float*>(smem + S::SUMS);
     float* sm_l = sm_m + kRowsWarps * NT * 8;
+    float2* sm_t = reinterpret_cast<float2*>(sm_l + kRowsWarps * NT * 8);   // of the joined warps
 
     const KvAttend& a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -233,9 +234,26 @@ kv_rows_kernel(const KvRowsArgs g)
     const int G = a.G;
     const int r0 = tile * NT * 8;   // first query row (row*G + head) of the tile
 
+    pdl_launch_dependents();   // kv_join_kernel gets ready meanwhile; it waits for all of this before it reads the parts
+
+    // The first tile's place does not wait for the lengths: what it finds beyond them is not used.
+    const int32_t* table = a.w.table + (UNION ? 0 : b * a.w.table_stride);
+    const int begin = split * g.s.chunk;
+    int to_issue = begin + 16 * warp;
+    auto union_at = [&](int at) { return lane < 16 && at + lane < a.M ? __ldg(a.uni + h * a.M + at + lane) : -1; };
+    auto place = [&](int pos) {
+        return pos >= 0 && (!UNION || pos < a.n) ? kv_page(a.c, table, a.w.table_pages, pos) : -1;
+    };
+    // All the ring's tiles at once, so that their loads do not wait for one another.
+    int pos[S::STAGES], page[S::STAGES];   // of tiles to come: their first token, or (union) their keys'
+#pragma unroll
+    for (int i = 0; i < S::STAGES; ++i) pos[i] = UNION ? union_at(to_issue + 16 * kRowsWarps * i) : to_issue + 16 * kRowsWarps * i;
+    int pos2 = UNION ? union_at(to_issue + 16 * kRowsWarps * S::STAGES) : 0;   // and of the one after them
+#pragma unroll
+    for (int i = 0; i < S::STAGES; ++i) page[i] = place(pos[i]);
+
     KvSpan sp;
     int keys;                       // of the tile's rows
-    const int32_t* table = a.w.table;
     if (UNION) {
         sp = KvSpan{0, 1, 0, 0};
         keys = static_cast<int>(min(static_cast<int64_t>(max(a.count[h], 0)), a.M));
@@ -243,9 +261,7 @@ kv_rows_kernel(const KvRowsArgs g)
         sp = kv_span(a, b);
         if (r0 >= sp.rows * G) return;
         keys = kv_tile_keys(a, sp, r0, NT * 8);
-        table += b * a.w.table_stride;
     }
-    const int begin = split * g.s.chunk;
     const int end = min(keys, begin + g.s.chunk);
     if (begin >= keys && split > 0) return;   // the join knows
 
@@ -257,17 +273,13 @@ kv_rows_kernel(const KvRowsArgs g)
     // and the exponent bytes of row lane % 16 of K (lanes below 16) or V
     const unsigned char* s_lane =
         CODED ? (lane < 16 ? a.c.ks : a.c.vs) + h * a.c.shead_stride + (UNION ? 0 : (lane & 15) * a.c.stoken_stride) : nullptr;
-    int pos1 = -1, pos2 = -1, page1 = -1;      // the next tile's page (union: key lane's, and the one's after it)
     int live_of[S::STAGES];                    // which keys of a held tile there are (kept in step with the ring)
     uint32_t sc[2] = {0, 0};                   // exponent bytes on their way
-    int to_issue = begin + 16 * warp, slot = 0;
+    int slot = 0;
     const uint32_t k_to = S::at(false, lr, lq), v_to = S::at(true, lr, lq);
 
-    auto union_at = [&](int at) { return lane < 16 && at + lane < end ? __ldg(a.uni + h * a.M + at + lane) : -1; };
-    auto place = [&](int pos) {
-        return pos >= 0 && (!UNION || pos < a.n) ? kv_page(a.c, table, a.w.table_pages, pos) : -1;
-    };
-    auto issue = [&]() {   // the tile at to_issue, into `slot`; the exponents of the one before to theirs
+    // The tile at to_issue, whose place is given, into `slot`; the exponents of the one before to theirs.
+    auto issue = [&](int pos1, int page1) {
         if (CODED) {
             const uint32_t at = ring + (slot == 0 ? S::STAGES - 1 : slot - 1) * S::STAGE + 32 * S::RB + lane * S::SBW;
             if (S::SBW == 4) asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(at), "r"(sc[0]) : "memory");
@@ -281,7 +293,7 @@ kv_rows_kernel(const KvRowsArgs g)
             const unsigned char *kp[S::RPL], *vp[S::RPL], *sp_;
             if (UNION) {
                 const int tok = pos1 & (a.c.page_tokens - 1);
-                live = static_cast<int>(__ballot_sync(0xffffffffu, page1 >= 0) & 0xffffu);
+                live = static_cast<int>(__ballot_sync(0xffffffffu, page1 >= 0 && at + lane < end) & 0xffffu);
                 const int64_t off = page1 >= 0 ? page1 * a.c.page_stride + tok * a.c.token_stride : 0;
                 const int64_t soff = CODED && page1 >= 0 ? page1 * a.c.spage_stride + tok * a.c.stoken_stride : 0;
 #pragma unroll
@@ -338,13 +350,6 @@ kv_rows_kernel(const KvRowsArgs g)
                     }
                 }
             }
-            if (UNION) {
-                pos1 = pos2;
-                page1 = place(pos1);
-                pos2 = union_at(at + 32 * kRowsWarps);
-            } else {
-                page1 = at + 16 * kRowsWarps < end ? place(at + 16 * kRowsWarps) : -1;
-            }
         }
         asm volatile("cp.async.commit_group;\n" ::: "memory");
 #pragma unroll
@@ -352,30 +357,31 @@ kv_rows_kernel(const KvRowsArgs g)
         live_of[S::STAGES - 1] = live;
         slot = slot + 1 == S::STAGES ? 0 : slot + 1;
     };
-    if (UNION) {
-        pos1 = union_at(to_issue);
-        pos2 = union_at(to_issue + 16 * kRowsWarps);
-    } else {
-        pos1 = to_issue < end ? to_issue : -1;
-    }
-    page1 = place(pos1);
 #pragma unroll
     for (int i = 0; i < S::STAGES; ++i) live_of[i] = 0;
-    for (int i = 0; i + 1 < S::STAGES; ++i) issue();
+#pragma unroll
+    for (int i = 0; i + 1 < S::STAGES; ++i) issue(pos[i], page[i]);
+    int pos1 = pos[S::STAGES - 1], page1 = page[S::STAGES - 1];   // of the next tile
 
     // ---- Q^T operand registers: lane (r, c) of step ks holds channels of row r that match K's.
-    auto query = [&](int qr, int d) {
-        if (qr >= sp.rows * G) return 0.0f;
-        const int64_t at = (sp.first + qr / G) * a.q_tok + (static_cast<int64_t>(h) * G + qr % G) * a.q_head + d;
-        return QT == FATHOM_KEYS_F32 ? static_cast<const float*>(a.q)[at]
-                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at]);
-    };
     for (int e = threadIdx.x; e < S::KS * NT * 32; e += kRowsThreads) {
         const int el = e & 31, nt = (e >> 5) % NT, ks = (e >> 5) / NT, qr = r0 + nt * 8 + (el >> 2);
-        uint32_t lo[S::NQ], hi[S::NQ];
         const int d = CODED ? (ks / S::KPW) * 4 * S::KPB + (el & 3) * S::KPB + (ks % S::KPW) * 4 : 16 * ks + 2 * (el & 3);
-        split2<S::NQ>(query(qr, d), query(qr, d + (CODED ? 2 : 1)), lo);
-        split2<S::NQ>(query(qr, d + (CODED ? 1 : 8)), query(qr, d + (CODED ? 3 : 9)), hi);
+        constexpr int D1 = CODED ? 2 : 1, D2 = CODED ? 1 : 8, D3 = CODED ? 3 : 9;
+        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (qr < sp.rows * G) {
+            const int tok = UNION ? 0 : qr / G;
+            const int64_t at = (sp.first + tok) * a.q_tok + (static_cast<int64_t>(h) * G + (qr - tok * G)) * a.q_head + d;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t from = at + (j == 0 ? 0 : j == 1 ? D1 : j == 2 ? D2 : D3);
+                x[j] = QT == FATHOM_KEYS_F32 ? static_cast<const float*>(a.q)[from]
+                                             : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[from]);
+            }
+        }
+        uint32_t lo[S::NQ], hi[S::NQ];
+        split2<S::NQ>(x[0], x[1], lo);
+        split2<S::NQ>(x[2], x[3], hi);
 #pragma unroll
         for (int p = 0; p < S::NQ; ++p) qf[((p * S::KS + ks) * NT + nt) * 32 + el] = make_uint2(lo[p], hi[p]);
     }
@@ -414,7 +420,11 @@ kv_rows_kernel(const KvRowsArgs g)
         asm volatile("cp.async.wait_group %0;\n" ::"n"(S::STAGES - 2) : "memory");
         __syncwarp();
         const int live = live_of[1];   // the oldest tile but the one just used up
-        issue();
+        const int next = to_issue + 16 * kRowsWarps;
+        issue(pos1, page1);
+        pos1 = UNION ? pos2 : next;
+        page1 = next < end ? place(pos1) : -1;
+        if (UNION) pos2 = union_at(next + 16 * kRowsWarps);
         const uint32_t here = ring + cur * S::STAGE;
         cur = cur + 1 == S::STAGES ? 0 : cur + 1;
 
@@ -563,20 +573,31 @@ kv_rows_kernel(const KvRowsArgs g)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float top = -INFINITY;
+            const int row = nt * 8 + 2 * c + i;
+            float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w * NT * 8 + nt * 8 + 2 * c + i]);
-            w8[nt][i] = exp2_fast(m[nt][i] - (top == -INFINITY ? 0.0f : top));
+            for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w * NT * 8 + row]);
+            const float low = top == -INFINITY ? 0.0f : top;
+            w8[nt][i] = exp2_fast(m[nt][i] - low);
+            if (warp == 0 && r == 0) {
+#pragma unroll
+                for (int w = 0; w < kRowsWarps; ++w) sum += sm_l[w * NT * 8 + row] * exp2_fast(sm_m[w * NT * 8 + row] - low);
+                sm_t[row] = make_float2(top, sum);
+            }
         }
-    for (int w = 0; w < kRowsWarps; ++w) {
-        if (warp == w) {
+    // The warps' sums side by side where the ring has room for them, else one after another in one place.
+    constexpr int SIDES = S::RING >= kRowsWarps * S::OB ? kRowsWarps : 1;
+    constexpr int SIDE = S::OB / sizeof(float);
+    for (int w = 0; w < kRowsWarps; w += SIDES) {
+        if (SIDES > 1 || warp == w) {
+            float* mine = os + (SIDES > 1 ? warp * SIDE : 0);
 #pragma unroll
             for (int t = 0; t < S::KS; ++t)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float* to = os + (nt * 8 + 2 * c + (i & 1)) * (D + 8) + (2 * t + (i >> 1)) * 8 + r;
+                        float* to = mine + (nt * 8 + 2 * c + (i & 1)) * (D + 8) + (2 * t + (i >> 1)) * 8 + r;
                         const float x = o[t][nt][i] * w8[nt][i & 1];
                         *to = w == 0 ? x : *to + x;
                     }
@@ -584,34 +605,32 @@ kv_rows_kernel(const KvRowsArgs g)
         __syncthreads();
     }
     const bool parts = g.s.splits > 1;
-    for (int e = threadIdx.x; e < NT * 8 * D; e += kRowsThreads) {
-        const int row = e / D, d = e % D;
+    for (int row = warp; row < NT * 8; row += kRowsWarps) {
         const int qr = r0 + row;
         if (qr >= sp.rows * G) break;
-        float top = -INFINITY, sum = 0.0f;
+        const float2 t = sm_t[row];   // maximum and weight sum
+        const int tok = UNION ? 0 : qr / G;
+        const int64_t head = ((sp.first + tok) * a.c.H + h) * G + (qr - tok * G), at_p = split * g.heads + head;
+        if (parts && lane == 0) {
+            g.pm[at_p] = t.x;
+            g.pl[at_p] = t.y;
+        }
 #pragma unroll
-        for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sm_m[w * NT * 8 + row]);
-        const float low = top == -INFINITY ? 0.0f : top;
+        for (int d = lane; d < D; d += 32) {
+            // with codes, channel d = 8 VPB q + VPB r + j is kept at (VPB q + j) 8 + r
+            const int at = row * (D + 8) + (CODED ? ((d / (8 * S::VPB)) * S::VPB + d % S::VPB) * 8 + (d / S::VPB) % 8 : d);
+            float x = os[at];
 #pragma unroll
-        for (int w = 0; w < kRowsWarps; ++w) sum += sm_l[w * NT * 8 + row] * exp2_fast(sm_m[w * NT * 8 + row] - low);
-        // with codes, channel d = 8 VPB q + VPB r + j is kept at (VPB q + j) 8 + r
-        const int kept = CODED ? ((d / (8 * S::VPB)) * S::VPB + d % S::VPB) * 8 + (d / S::VPB) % 8 : d;
-        const float x = os[row * (D + 8) + kept];
-        const int64_t head = ((sp.first + qr / G) * a.c.H + h) * G + qr % G;
-        if (parts) {
-            const int64_t at_p = split * g.heads + head;
-            g.po[at_p * D + d] = x;
-            if (d == 0) {
-                g.pm[at_p] = top;
-                g.pl[at_p] = sum;
+            for (int w = 1; w < SIDES; ++w) x += os[w * SIDE + at];
+            if (parts) {
+                g.po[at_p * D + d] = x;
+            } else {
+                const float y = t.y == 0.0f ? 0.0f : x / t.y;   // no token was seen (NaN scores make the sum NaN)
+                if (QT == FATHOM_KEYS_F32) static_cast<float*>(a.out)[head * D + d] = y;
+                else static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16(y);
             }
-        } else {
-            const float y = sum == 0.0f ? 0.0f : x / sum;   // no token was seen (NaN scores make the sum NaN)
-            if (QT == FATHOM_KEYS_F32) static_cast<float*>(a.out)[head * D + d] = y;
-            else static_cast<__nv_bfloat16*>(a.out)[head * D + d] = __float2bfloat16(y);
         }
     }
-    pdl_launch_dependents();
 }
 
 template <int D, int FMT, int QT, int NT, bool UNION>
