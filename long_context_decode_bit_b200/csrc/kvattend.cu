@@ -39,7 +39,10 @@ KvSplit rows_split(int H, int G, int D, int64_t rows, int B, int64_t max_new, in
 {
     KvSplit s{};
     const int64_t qrows = max_new * G, len = std::max<int64_t>(max_len, 1);
-    const bool chunk = q_dtype == FATHOM_KEYS_BF16 && (D == 64 || D == 128) && qrows > 64;
+    // kvchunk.cuh takes bf16 queries from 33 rows (heads of tokens) on.  One session of 8 groups, 32k int8 tokens, 128
+    // channels: 16 rows 45 us there and 44 here, 32 rows 46 and 46, 64 rows 50 and 73, 128 rows 57 and 116; eight
+    // sessions of up to 8k bf16 tokens: 16 rows 66 and 73, 32 rows 66 and 77, 64 rows 70 and 122.
+    const bool chunk = q_dtype == FATHOM_KEYS_BF16 && D <= 128 && qrows > 32;
     s.nt = chunk ? 0 : (qrows <= 8 ? 1 : (D <= 128 ? 4 : 2));
     s.tile_rows = chunk ? kChunkRows : 8 * s.nt;
     s.row_tiles = static_cast<int32_t>(ceil_div(qrows, s.tile_rows));

@@ -1,5 +1,6 @@
 // Attention of prompt chunks over the paged cache on the tensor memory's
-// matrix units (tcgen05): bf16 queries, 64 or 128 channels.
+// matrix units (tcgen05): bf16 queries, up to 128 channels (32 and 96 as 64
+// and 128 with zeros behind).
 //
 // A CTA takes 256 query rows (a row is one head of one token; the G heads of
 // a group lie next to each other, so they share every cached byte) as two
@@ -210,7 +211,8 @@ __device__ __forceinline__ int64_t chunk_off(const KvCache& c, int page, int at,
 }
 
 // The whole 128-token tiles of K and V from `begin` on, in the order K0 V0 K1 V1 ..., into the ring.
-template <int D, int FMT>
+// D is the width of the operands, c.D (less where not FULL) that of the rows.
+template <int D, int FMT, bool FULL>
 __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* table, int table_pages, int h, int begin, int end,
                                            uint32_t ring, uint32_t full, uint32_t empty)
 {
@@ -223,13 +225,14 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
         constexpr int PIECES = D / 8, ROWS = 128 / PIECES;   // rows of a pass
         constexpr int AHEAD = S::STAGES - 2;                 // stages that may be on their way
         const int piece = t % PIECES, r0 = t / PIECES;
+        const bool there = FULL || piece * 8 < c.D;
         const uint32_t to0 = ring + tile_at(r0, piece);      // rows behind: the same place in the swizzle, ROWS being 8 or 16
         const int64_t row_off = r0 * c.token_stride + piece * 16;
         int i = 0;
         for (int j = 0; j < tiles && ok; ++j) {
             const int at = begin + j * kChunkKeys;
             const int64_t off = chunk_off(c, page, at, h, lane);
-            const bool whole = end - at >= kChunkKeys && __ballot_sync(0xffffffffu, page >= 0) == 0xff;
+            const bool whole = FULL && end - at >= kChunkKeys && __ballot_sync(0xffffffffu, page >= 0) == 0xff;
             page = chunk_page(c, table, table_pages, at + kChunkKeys, end, lane);
             for (int s = 0; s < 2; ++s, ++i) {
                 const int st = i % S::STAGES;
@@ -244,7 +247,7 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
                     if (whole) {
                         cp_async16_to(to, from);
                     } else {
-                        const bool live = o >= 0 && at + r0 + p * ROWS < end;
+                        const bool live = there && o >= 0 && at + r0 + p * ROWS < end;
                         cp_async16_to(to, live ? from : data, live ? 16 : 0);
                     }
                 }
@@ -272,7 +275,7 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
         const CodeMasks masks = code_masks<FMT>();
         const uint32_t mine = ring + S::STAGES * S::TILE + t * 16;
         const int64_t row_off = (lr & 15) * c.token_stride + lq * 16;
-        const int64_t row_soff = (lr & 15) * c.stoken_stride + (D == 64 ? lq >> 1 : 0);
+        const int64_t row_soff = (lr & 15) * c.stoken_stride + (FULL && D == 64 ? lq >> 1 : 0);
         const int stages = 2 * tiles;
         int is = 0, at = begin;
         int64_t off = -1, soff = 0;
@@ -296,11 +299,19 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
                     const bool live = o >= 0 && at + lr + 32 * i < end;
                     const unsigned char* from = live ? data + o + row_off : data;
 #pragma unroll
-                    for (int k = 0; k < KP; ++k) cp_async16_to(slot + (i * KP + k) * 2048, from + 64 * k, live ? 16 : 0);
+                    for (int k = 0; k < KP; ++k) {
+                        const bool there = live && (FULL || (lq + 4 * k) * 16 < c.D);
+                        cp_async16_to(slot + (i * KP + k) * 2048, there ? from + 64 * k : data, there ? 16 : 0);
+                    }
                     sc[i] = 0;
                     if (live) {
                         const unsigned char* sp = scale + so + row_soff;
-                        sc[i] = D == 128 ? __ldg(reinterpret_cast<const uint32_t*>(sp)) : __ldg(sp);
+                        if (!FULL) {   // one block of 64, or three of 128 channels
+                            sc[i] = __ldg(sp);
+                            if (D == 128) sc[i] |= static_cast<uint32_t>(__ldg(sp + 1)) << 8 | static_cast<uint32_t>(__ldg(sp + 2)) << 16;
+                        } else {
+                            sc[i] = D == 128 ? __ldg(reinterpret_cast<const uint32_t*>(sp)) : __ldg(sp);
+                        }
                     }
                 }
             }
@@ -341,7 +352,7 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
     return ok;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool FULL>
 __global__ void __launch_bounds__(kChunkThreads, 1)
 kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
 {
@@ -466,23 +477,24 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
         __syncwarp();
     } else if (warp >= 8) {
         regs_down<kRegsLoad>();
-        if (!chunk_load<D, FMT>(a.c, table, a.w.table_pages, h, begin, end, ring, full, empty)) atomicOr(fault, kFaultTimeout);
+        if (!chunk_load<D, FMT, FULL>(a.c, table, a.w.table_pages, h, begin, end, ring, full, empty)) atomicOr(fault, kFaultTimeout);
     } else {
         regs_up<kRegsSoftmax>();
         {   // Q, by both row tiles' warps
             constexpr int PIECES = D / 8, ROWS = 256 / PIECES;
             const int piece = threadIdx.x % PIECES, at_row = threadIdx.x / PIECES;
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(h) * G * a.q_head + piece * 8;
+            const bool wide = FULL || piece * 8 < a.c.D;
             const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // the softmax uses |scale|
             const bool vec = flip == 0 && ((reinterpret_cast<uintptr_t>(q) & 15) | (a.q_tok & 7) | (a.q_head & 7)) == 0;
 #pragma unroll 4
             for (int row = at_row; row < kChunkRows; row += ROWS) {
                 const unsigned qr = min(r0 + row, nrows - 1), tok = qr / static_cast<unsigned>(G), g1 = qr - tok * G;
-                const bool there = r0 + row < nrows;
+                const bool there = wide && r0 + row < nrows;
                 const uint32_t to = q_s + (row >> 7) * S::TILE + tile_at(row & 127, piece);
                 const __nv_bfloat16* from = q + (sp.first + tok) * a.q_tok + g1 * a.q_head;
                 if (vec) {
-                    cp_async16_to(to, from, there ? 16 : 0);
+                    cp_async16_to(to, there ? from : static_cast<const __nv_bfloat16*>(a.q), there ? 16 : 0);
                 } else {
                     uint32_t w[4];
 #pragma unroll
@@ -584,12 +596,14 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                 if (lane == 0) atomicOr(fault, kFaultTimeout);
             } else {
                 const int64_t head = ((sp.first + qr / G) * a.c.H + h) * G + qr % G;
+                const int64_t width = FULL ? D : a.c.D;
                 const bool parts = g.s.splits > 1;
                 const float f = parts ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f);
                 const int64_t at_p = split * g.heads + head;
                 const bool nothing = l == 0.0f;   // no token was seen (NaN scores make l NaN)
 #pragma unroll
                 for (int i = 0; i < D; i += 32) {
+                    if (!FULL && i >= a.c.D) break;
                     float o[32];
                     if (tiles > 0) {
                         tmem_ld32(o_at + i, o);
@@ -599,11 +613,11 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                     for (int k = 0; k < 32; ++k) o[k] = nothing ? 0.0f : o[k] * f;
                     if (qr < nrows) {
                         if (parts) {
-                            float* to = g.po + at_p * D + i;
+                            float* to = g.po + at_p * width + i;
 #pragma unroll
                             for (int k = 0; k < 32; k += 8) st_global32(to + k, reinterpret_cast<const uint32_t*>(o + k));
                         } else {
-                            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + head * D + i;
+                            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + head * width + i;
                             if ((reinterpret_cast<uintptr_t>(a.out) & 31) == 0) {
                                 uint32_t w[16];
 #pragma unroll
@@ -632,11 +646,11 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
     }
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool FULL>
 int launch_chunk_t(const KvRowsArgs& g, cudaStream_t stream)
 {
     using S = ChunkShape<D, FMT>;
-    const void* f = reinterpret_cast<const void*>(kv_chunk_kernel<D, FMT>);
+    const void* f = reinterpret_cast<const void*>(kv_chunk_kernel<D, FMT, FULL>);
     // The roles' registers must add up to no more than the block is launched with, or the softmax waits for ever.
     static const int launch_regs = [f] {
         cudaFuncAttributes attr;
@@ -650,11 +664,11 @@ int launch_chunk_t(const KvRowsArgs& g, cudaStream_t stream)
     if (st) return st;
     const dim3 grid(static_cast<unsigned>(g.s.splits) * g.s.row_tiles, static_cast<unsigned>(g.a.c.H),
                     static_cast<unsigned>(g.a.w.B));
-    kv_chunk_kernel<D, FMT><<<grid, kChunkThreads, S::SMEM, stream>>>(g, fault);
+    kv_chunk_kernel<D, FMT, FULL><<<grid, kChunkThreads, S::SMEM, stream>>>(g, fault);
     return launch_status();
 }
 
-// kvchunk.cu: chunks of bf16 queries over caches of 64 or 128 channels.
+// kvchunk.cu: chunks of bf16 queries over caches of up to 128 channels.
 int launch_chunk(const KvRowsArgs& g, int format, cudaStream_t stream);
 
 }  // namespace fathom

@@ -45,6 +45,24 @@ def test_edges_of_tiles(fathom_gpu, fmt, causal, H, G, D, page, lens):
     both(fathom_gpu, cache, fmt, q, table, cu, length, max(n for n, _ in lens), max(t for _, t in lens), causal)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("layout", ["head", "token", "layer"])
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("H,G,D,page,lens", [(2, 4, 96, 64, [(60, 500), (20, 129)]), (3, 5, 32, 16, [(130, 999)]),
+                                             (1, 1, 96, 16, [(300, 300), (1, 5000)]), (1, 3, 32, 256, [(33, 3000), (40, 40)])])
+def test_widths_between(fathom_gpu, fmt, causal, layout, H, G, D, page, lens):
+    """32 and 96 channels, taken as 64 and 128 with zeros behind: what lies behind a row in the cache is not used."""
+    pages, table, cu, length = make_batch(lens, page, seed=D)
+    cache = make_cache(fathom_gpu, fmt, pages, H, D, page, layout)
+    if fmt != "bf16":
+        cache.k_scale.fill_(255), cache.v_scale.fill_(255)
+    else:
+        cache.k.fill_(float("nan")), cache.v.fill_(float("nan"))
+    fill(fathom_gpu, cache, lens, table, seed=G)
+    q = queries((int(cu[-1]), H * G, D), 4)
+    both(fathom_gpu, cache, fmt, q, table, cu, length, max(n for n, _ in lens), max(t for _, t in lens), causal)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "int8"])
 @pytest.mark.parametrize("D", [64, 128])
 def test_maximum_that_keeps_growing(fathom_gpu, fmt, D):
