@@ -105,7 +105,7 @@ int check_row_ptrs(const fathom_kv_rows* w, KvRows* out)
 
 bool dtype_ok(int t) { return t == FATHOM_KEYS_F32 || t == FATHOM_KEYS_BF16; }
 size_t dtype_bytes(int t) { return t == FATHOM_KEYS_F32 ? 4 : 2; }
-bool scale_ok(float s) { return s == s && s <= 3.0e38f && s >= -3.0e38f; }
+bool scale_ok(float s) { return s <= 1.0e38f && s >= -1.0e38f; }   // times log2 e it is finite too; false for NaN
 
 }  // namespace
 }  // namespace fathom
@@ -181,6 +181,7 @@ int fathom_paged_attention(const fathom_kv_cache* cache, const fathom_kv_rows* r
     if (G < 1 || G > kMaxG) return FATHOM_ERR_UNSUPPORTED;
     if (cache->H == 0 || rows->B == 0 || rows->rows == 0 || max_new == 0) return FATHOM_OK;
     if (max_new > rows->rows) max_new = rows->rows;
+    if (max_new * G >= (1LL << 31)) return FATHOM_ERR_UNSUPPORTED;
     const size_t need = fathom_paged_attention_workspace_bytes(cache->H, G, cache->D, rows->rows, rows->B, max_new,
                                                                max_len, q_dtype);
     if (ws_bytes < need) return FATHOM_ERR_WORKSPACE;

@@ -42,9 +42,9 @@ KvSplit rows_split(int H, int G, int D, int64_t rows, int B, int64_t max_new, in
     // kvchunk.cuh takes bf16 queries from 33 rows (heads of tokens) on.  One session of 8 groups, 32k int8 tokens, 128
     // channels: 16 rows 45 us there and 44 here, 32 rows 46 and 46, 64 rows 50 and 73, 128 rows 57 and 116; eight
     // sessions of up to 8k bf16 tokens: 16 rows 66 and 73, 32 rows 66 and 77, 64 rows 70 and 122.
-    const bool chunk = q_dtype == FATHOM_KEYS_BF16 && D <= 128 && qrows > 32;
+    const bool chunk = q_dtype == FATHOM_KEYS_BF16 && qrows > 32;
     s.nt = chunk ? 0 : (qrows <= 8 ? 1 : (D <= 128 ? 4 : 2));
-    s.tile_rows = chunk ? kChunkRows : 8 * s.nt;
+    s.tile_rows = chunk ? chunk_rows(D) : 8 * s.nt;
     s.row_tiles = static_cast<int32_t>(ceil_div(qrows, s.tile_rows));
     if (s.nt == 1) {
         // Single tokens.  Four CTAs fit an SM.  One session: its stretches are equal, one wave of CTAs.  Several of
@@ -56,10 +56,10 @@ KvSplit rows_split(int H, int G, int D, int64_t rows, int B, int64_t max_new, in
         // A batch has no more row tiles than all its rows fill, and one begun by each sequence.
         const int64_t items = H * std::min(static_cast<int64_t>(B) * s.row_tiles, ceil_div(rows * G, s.tile_rows) + B - 1);
         const int64_t longest = std::min(items, static_cast<int64_t>(H) * s.row_tiles), heads = rows * H * G;
-        // A CTA to an SM and 128 tokens in 1.7 us, or two and 64 tokens in 1.5.
-        const int64_t tile = chunk ? kChunkKeys : 16 * kRowsWarps;
+        // A CTA to an SM and 128 tokens in 1.7 us (64 in 1.0 beyond 128 channels), or two and 64 tokens in 1.5.
+        const int64_t tile = chunk ? chunk_keys(D) : 16 * kRowsWarps;
         s.chunk = static_cast<int32_t>(tile * cut(ceil_div(len, tile), items, longest, heads, D, chunk ? kSms : 2 * kSms,
-                                                  chunk ? 1.7 : 1.5, chunk ? 5 : 4));
+                                                  !chunk ? 1.5 : D <= 128 ? 1.7 : 1.0, !chunk ? 4 : D <= 128 ? 5 : 9));
     }
     s.splits = static_cast<int32_t>(ceil_div(len, s.chunk));
     return s;

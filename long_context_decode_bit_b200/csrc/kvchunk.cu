@@ -23,7 +23,9 @@ int launch_chunk(const KvRowsArgs& g, int format, cudaStream_t stream)
         case 32: return launch_chunk_d<64, false>(g, format, stream);
         case 64: return launch_chunk_d<64, true>(g, format, stream);
         case 96: return launch_chunk_d<128, false>(g, format, stream);
-        default: return launch_chunk_d<128, true>(g, format, stream);
+        case 128: return launch_chunk_d<128, true>(g, format, stream);
+        case 256: return launch_chunk_d<256, true>(g, format, stream);
+        default: return launch_chunk_d<256, false>(g, format, stream);   // 160, 192, 224
     }
 }
 

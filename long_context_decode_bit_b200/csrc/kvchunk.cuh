@@ -1,11 +1,12 @@
 // Attention of prompt chunks over the paged cache on the tensor memory's
-// matrix units (tcgen05): bf16 queries, up to 128 channels (32 and 96 as 64
-// and 128 with zeros behind).
+// matrix units (tcgen05): bf16 queries, 64, 128 or 256 channels and, with
+// zeros behind, the widths between.
 //
 // A CTA takes 256 query rows (a row is one head of one token; the G heads of
 // a group lie next to each other, so they share every cached byte) as two
-// tiles of 128, and the tokens of one stretch in tiles of 128.  Per tile of
-// tokens and of rows
+// tiles of 128, and the tokens of one stretch in tiles of 128; beyond 128
+// channels, whose O leaves no room for a second, one tile of rows and tiles
+// of 64 tokens, which take the same shared memory.  Per tile of tokens and of rows
 //   S [128 x 128] = Q K^T  (both in shared memory, accumulators in tensor memory),
 //   P = 2^(S scale log2 e - m), l += row sums,
 //   O [128 x D] += P V     (P in tensor memory over S, V in shared memory).
@@ -35,8 +36,9 @@
 namespace fathom {
 
 constexpr int kChunkThreads = 512;
-constexpr int kChunkRows = 256;   // query rows of a CTA
-constexpr int kChunkKeys = 128;   // tokens of a tile
+// Query rows of a CTA and tokens of a tile, by the width of a row.
+constexpr int chunk_rows(int D) { return D <= 128 ? 256 : 128; }
+constexpr int chunk_keys(int D) { return D <= 128 ? 128 : 64; }
 // Registers a thread of each role keeps; their sum is the launch's 4 x 128.
 constexpr int kRegsSoftmax = 192, kRegsLoad = 80, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 512, "more registers than the block has");
@@ -44,14 +46,19 @@ static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 512, "more registers 
 template <int D, int FMT>
 struct ChunkShape {
     static constexpr bool CODED = FMT != FATHOM_KV_BF16;
+    static constexpr bool PAIR = D <= 128;                        // two row tiles in turn, or two tiles of tokens of one
+    static constexpr int ROWS = chunk_rows(D), KEYS = chunk_keys(D);
     static constexpr int DB = D / 64;                             // 64-channel blocks of a row
-    static constexpr int TILE = kChunkKeys * 128 * DB;            // bytes of 128 rows
-    static constexpr int STAGES = D == 128 ? (CODED ? 3 : 5) : (CODED ? 6 : 8);   // tiles of K or V held as operands
-    static constexpr int RAWS = CODED ? (D == 128 ? 3 : 4) : 0;   // and as they come
-    static constexpr int RAW = kChunkKeys * D + 2048;             // codes, and exponents in 16 bytes a thread
-    static constexpr int QB = 2 * TILE;
+    static constexpr int QTILE = 128 * 128 * DB;                  // bytes of 128 rows of Q
+    static constexpr int TILE = KEYS * 128 * DB;                  // and of a tile of K or V
+    static constexpr int STAGES = D == 64 ? (CODED ? 6 : 8) : (CODED ? 3 : 5);   // tiles of K or V held as operands
+    static constexpr int RAWS = CODED ? (D == 64 ? 4 : 3) : 0;    // and as they come
+    static constexpr int RAW = KEYS * D + 2048;                   // codes, and exponents in 16 bytes a thread
+    static constexpr int QB = (ROWS / 128) * QTILE;
     static constexpr size_t BARS = QB + static_cast<size_t>(STAGES) * TILE + static_cast<size_t>(RAWS) * RAW;
     static constexpr size_t SMEM = BARS + 256 + 1024;             // the base is moved up to a multiple of 1024
+    static_assert(SMEM <= 227 * 1024, "fits an SM, and only once");
+    static_assert(SMEM > 114 * 1024, "a CTA has the SM's tensor memory to itself");
 };
 
 // ---- tensor memory and its products (cta_group::1)
@@ -186,10 +193,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 
 // ---- bringing K and V
 
-// 16-byte piece `piece` (of D/8) of row `row` of a tile.
+// 16-byte piece `piece` (of D/8) of row `row` of a tile of ROWS rows.
+template <int ROWS>
 __device__ __forceinline__ uint32_t tile_at(int row, int piece)
 {
-    return (piece >> 3) * (kChunkKeys * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+    return (piece >> 3) * (ROWS * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint4 x)
@@ -210,15 +218,17 @@ __device__ __forceinline__ int64_t chunk_off(const KvCache& c, int page, int at,
     return page < 0 ? -1 : kv_off(c, page, h, (at + 16 * lane) & (c.page_tokens - 1));
 }
 
-// The whole 128-token tiles of K and V from `begin` on, in the order K0 V0 K1 V1 ..., into the ring.
+// The whole tiles of K and V from `begin` on, in the order K0 V0 K1 V1 ..., into the ring.
 // D is the width of the operands, c.D (less where not FULL) that of the rows.
 template <int D, int FMT, bool FULL>
 __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* table, int table_pages, int h, int begin, int end,
                                            uint32_t ring, uint32_t full, uint32_t empty)
 {
     using S = ChunkShape<D, FMT>;
+    constexpr int KEYS = S::KEYS;
+    constexpr uint32_t ALL = (1u << (KEYS / 16)) - 1;
     const int t = threadIdx.x & 127, lane = threadIdx.x & 31;
-    const int tiles = (end - begin + kChunkKeys - 1) / kChunkKeys;
+    const int tiles = (end - begin + KEYS - 1) / KEYS;
     bool ok = true;
     int page = chunk_page(c, table, table_pages, begin, end, lane);
     if constexpr (FMT == FATHOM_KV_BF16) {
@@ -226,24 +236,25 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
         constexpr int AHEAD = S::STAGES - 2;                 // stages that may be on their way
         const int piece = t % PIECES, r0 = t / PIECES;
         const bool there = FULL || piece * 8 < c.D;
-        const uint32_t to0 = ring + tile_at(r0, piece);      // rows behind: the same place in the swizzle, ROWS being 8 or 16
+        const uint32_t to0 = ring + tile_at<KEYS>(r0, piece);
         const int64_t row_off = r0 * c.token_stride + piece * 16;
         int i = 0;
         for (int j = 0; j < tiles && ok; ++j) {
-            const int at = begin + j * kChunkKeys;
+            const int at = begin + j * KEYS;
             const int64_t off = chunk_off(c, page, at, h, lane);
-            const bool whole = FULL && end - at >= kChunkKeys && __ballot_sync(0xffffffffu, page >= 0) == 0xff;
-            page = chunk_page(c, table, table_pages, at + kChunkKeys, end, lane);
+            const bool whole = FULL && end - at >= KEYS && (__ballot_sync(0xffffffffu, page >= 0) & ALL) == ALL;
+            page = chunk_page(c, table, table_pages, at + KEYS, end, lane);
             for (int s = 0; s < 2; ++s, ++i) {
                 const int st = i % S::STAGES;
                 ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((i / S::STAGES) & 1) ^ 1));
                 if (!ok) break;
                 const unsigned char* data = s ? c.v : c.k;
 #pragma unroll
-                for (int p = 0; p < 128 / ROWS; ++p) {
+                for (int p = 0; p < KEYS / ROWS; ++p) {
                     const int64_t o = __shfl_sync(0xffffffffu, off, p * ROWS >> 4);
                     const unsigned char* from = data + o + row_off + (p * ROWS & 15) * c.token_stride;
-                    const uint32_t to = to0 + st * S::TILE + p * ROWS * 128;
+                    // p*ROWS rows behind; where ROWS is 4, every other time 4 chunks on in the swizzle
+                    const uint32_t to = ((to0 + st * S::TILE) ^ ((p * ROWS & 7) << 4)) + p * ROWS * 128;
                     if (whole) {
                         cp_async16_to(to, from);
                     } else {
@@ -268,9 +279,8 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
         if (ok)
             for (int k = max(1, i - AHEAD); k < i; ++k) mbar_arrive(full + 8 * (k % S::STAGES));
     } else {
-        // A thread copies 16-code pieces lq, lq + 4 of the rows lr, lr + 32, lr + 64, lr + 96 to a place of its own
-        // some tiles ahead, and decodes those same pieces from there.
-        constexpr int KP = D / 64, AHEAD = S::RAWS - 1;
+        // A thread copies 16-code pieces lq, lq + 4, ... of the rows lr, lr + 32, ... to a place of its own some tiles ahead, and decodes those same pieces from there.
+        constexpr int KP = D / 64, RP = KEYS / 32, SW = 4 / RP, AHEAD = S::RAWS - 1;   // SW words of exponents to a row
         const int lr = t >> 2, lq = t & 3, group = lr >> 4;
         const CodeMasks masks = code_masks<FMT>();
         const uint32_t mine = ring + S::STAGES * S::TILE + t * 16;
@@ -283,18 +293,18 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
         auto issue = [&]() {
             const uint32_t slot = mine + (is % S::RAWS) * S::RAW;
             if (is > 0)
-                st_shared16(mine + ((is - 1) % S::RAWS) * S::RAW + 4 * KP * 2048, make_uint4(sc[0], sc[1], sc[2], sc[3]));
+                st_shared16(mine + ((is - 1) % S::RAWS) * S::RAW + RP * KP * 2048, make_uint4(sc[0], sc[1], sc[2], sc[3]));
             if (is < stages) {
                 if ((is & 1) == 0) {
-                    at = begin + (is >> 1) * kChunkKeys;
+                    at = begin + (is >> 1) * KEYS;
                     off = chunk_off(c, page, at, h, lane);
                     soff = page < 0 ? 0 : kv_scale_off(c, page, h, (at + 16 * lane) & (c.page_tokens - 1));
-                    page = chunk_page(c, table, table_pages, at + kChunkKeys, end, lane);
+                    page = chunk_page(c, table, table_pages, at + KEYS, end, lane);
                 }
                 const unsigned char* data = (is & 1) ? c.v : c.k;
                 const unsigned char* scale = (is & 1) ? c.vs : c.ks;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < RP; ++i) {
                     const int64_t o = __shfl_sync(0xffffffffu, off, group + 2 * i), so = __shfl_sync(0xffffffffu, soff, group + 2 * i);
                     const bool live = o >= 0 && at + lr + 32 * i < end;
                     const unsigned char* from = live ? data + o + row_off : data;
@@ -303,14 +313,19 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
                         const bool there = live && (FULL || (lq + 4 * k) * 16 < c.D);
                         cp_async16_to(slot + (i * KP + k) * 2048, there ? from + 64 * k : data, there ? 16 : 0);
                     }
-                    sc[i] = 0;
+#pragma unroll
+                    for (int n = 0; n < SW; ++n) sc[SW * i + n] = 0;
                     if (live) {
                         const unsigned char* sp = scale + so + row_soff;
-                        if (!FULL) {   // one block of 64, or three of 128 channels
+                        if (FULL && D >= 128) {
+#pragma unroll
+                            for (int n = 0; n < SW; ++n) sc[SW * i + n] = __ldg(reinterpret_cast<const uint32_t*>(sp) + n);
+                        } else if (D == 64) {
                             sc[i] = __ldg(sp);
-                            if (D == 128) sc[i] |= static_cast<uint32_t>(__ldg(sp + 1)) << 8 | static_cast<uint32_t>(__ldg(sp + 2)) << 16;
                         } else {
-                            sc[i] = D == 128 ? __ldg(reinterpret_cast<const uint32_t*>(sp)) : __ldg(sp);
+#pragma unroll
+                            for (int n = 0; n < D / kKvBlock; ++n)
+                                if (n * kKvBlock < c.D) sc[SW * i + (n >> 2)] |= static_cast<uint32_t>(__ldg(sp + n)) << (8 * (n & 3));
                         }
                     }
                 }
@@ -326,19 +341,19 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
             const int st = i % S::STAGES;
             ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ((i / S::STAGES) & 1) ^ 1));
             if (!ok) break;
-            const uint32_t from = mine + (i % S::RAWS) * S::RAW, to = ring + st * S::TILE + tile_at(lr, 2 * lq);
+            const uint32_t from = mine + (i % S::RAWS) * S::RAW, to = ring + st * S::TILE + tile_at<KEYS>(lr, 2 * lq);
             uint32_t ps[4];
-            lds_words<4>(from + 4 * KP * 2048, ps);
+            lds_words<4>(from + RP * KP * 2048, ps);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < RP; ++r)
 #pragma unroll
                 for (int k = 0; k < KP; ++k) {
                     uint32_t w[4];
                     lds_words<4>(from + (r * KP + k) * 2048, w);
-                    const uint32_t byte = D == 128 ? (ps[r] >> (16 * k + 8 * (lq >> 1))) & 0xff : ps[r];
+                    const uint32_t byte = D == 64 ? ps[r] : (ps[SW * r + (k >> 1)] >> (16 * (k & 1) + 8 * (lq >> 1))) & 0xff;
                     const uint32_t f = pow_bits<FMT>(byte) * 0x10001u;
                     // the row's two 16-byte pieces, the second one chunk on in the swizzle
-                    const uint32_t there = to + r * 32 * 128 + k * (kChunkKeys * 128);
+                    const uint32_t there = to + r * 32 * 128 + k * (KEYS * 128);
                     st_shared16(there, make_uint4(decode2<FMT, 0, 1>(w[0], w[0], f, masks), decode2<FMT, 2, 3>(w[0], w[0], f, masks),
                                                   decode2<FMT, 0, 1>(w[1], w[1], f, masks), decode2<FMT, 2, 3>(w[1], w[1], f, masks)));
                     st_shared16(there ^ 16, make_uint4(decode2<FMT, 0, 1>(w[2], w[2], f, masks), decode2<FMT, 2, 3>(w[2], w[2], f, masks),
@@ -357,7 +372,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
 {
     using S = ChunkShape<D, FMT>;
-    constexpr int ST = S::STAGES;
+    constexpr int ST = S::STAGES, KEYS = S::KEYS;
+    constexpr uint32_t ALL = (1u << (KEYS / 16)) - 1;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const uint32_t q_s = smem_addr(base), ring = q_s + S::QB, bars = q_s + static_cast<uint32_t>(S::BARS);
@@ -372,15 +388,15 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
     const int h = blockIdx.y, b = blockIdx.z, G = a.G;
     // Later rows see more tokens: they start first.
     const int tile = g.s.row_tiles - 1 - static_cast<int>(blockIdx.x % g.s.row_tiles), split = blockIdx.x / g.s.row_tiles;
-    const int r0 = tile * kChunkRows;
+    const int r0 = tile * S::ROWS;
     const KvSpan sp = kv_span(a, b);
     const int nrows = sp.rows * G;
     if (r0 >= nrows) return;
-    const int keys = kv_tile_keys(a, sp, r0, kChunkRows);
+    const int keys = kv_tile_keys(a, sp, r0, S::ROWS);
     const int begin = split * g.s.chunk, end = min(keys, begin + g.s.chunk);
     if (begin >= keys && split > 0) return;   // the join knows
-    const int tiles = (max(end - begin, 0) + kChunkKeys - 1) / kChunkKeys;
-    const bool two = r0 + 128 < nrows;        // the second row tile has rows
+    const int tiles = (max(end - begin, 0) + KEYS - 1) / KEYS;
+    const bool two = S::PAIR && r0 + 128 < nrows;   // the second row tile has rows
     const int32_t* table = a.w.table + b * a.w.table_stride;
 
     if (warp == 12) {
@@ -412,26 +428,27 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
         if (warp == 12 && tiles > 0) {
             // The whole warp goes along, so that operands are in uniform registers; one lane issues.  (A lane on its own
             // took 90 cycles to a product, more than the product.)
-            constexpr uint32_t shape_s = tc_shape(kChunkKeys, false), shape_o = tc_shape(D, true);
+            constexpr uint32_t shape_s = tc_shape(KEYS, false), shape_o = tc_shape(D, true);
             auto scores = [&](int t, int st) {
-                const uint64_t q = tc_operand(q_s + t * S::TILE, 0), k = tc_operand(ring + st * S::TILE, 0);
+                const uint64_t q = tc_operand(q_s + (S::PAIR ? t * S::QTILE : 0), 0), k = tc_operand(ring + st * S::TILE, 0);
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = ((ks >> 2) * (kChunkKeys * 128) + (ks & 3) * 32) >> 4;
-                        tc_mma_ss(tmem + 128 * t, q + off, k + off, shape_s, ks > 0);
+                        const uint32_t off = (ks & 3) * 32 >> 4;
+                        tc_mma_ss(tmem + 128 * t, q + ((ks >> 2) * (128 * 128) >> 4) + off, k + ((ks >> 2) * (KEYS * 128) >> 4) + off,
+                                  shape_s, ks > 0);
                     }
                     tc_commit(s_full + 8 * t);
                 }
                 __syncwarp();
             };
             auto values = [&](int t, int st, int half, bool add) {
-                const uint64_t v = tc_operand(ring + st * S::TILE + half * (kChunkKeys / 2) * 128, kChunkKeys * 128);
-                const uint32_t p = tmem + 128 * t + half * (kChunkKeys / 4);
+                const uint64_t v = tc_operand(ring + st * S::TILE + half * (KEYS / 2) * 128, KEYS * 128);
+                const uint32_t p = tmem + 128 * t + half * (KEYS / 4);
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < kChunkKeys / 32; ++ks)
-                        tc_mma_ts(tmem + 256 + 128 * t, p + 8 * ks, v + ks * (2048 >> 4), shape_o, add || ks > 0);
+                    for (int ks = 0; ks < KEYS / 32; ++ks)
+                        tc_mma_ts(tmem + 256 + (S::PAIR ? 128 * t : 0), p + 8 * ks, v + ks * (2048 >> 4), shape_o, add || ks > 0);
                 }
                 __syncwarp();
             };
@@ -447,27 +464,51 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                 for (int t = 0; t < nt; ++t) scores(t, 0);
                 done(empty);
             }
-            for (int j = 0; j < tiles && ok; ++j) {
-                const int iv = 2 * j + 1, ik = iv + 1;
-                const bool more = j + 1 < tiles;
-                ok = wait(full + 8 * (iv % ST), (iv / ST) & 1);
-                for (int t = 0; t < nt && ok; ++t) {
+            if constexpr (S::PAIR) {
+                for (int j = 0; j < tiles && ok; ++j) {
+                    const int iv = 2 * j + 1, ik = iv + 1;
+                    const bool more = j + 1 < tiles;
+                    ok = wait(full + 8 * (iv % ST), (iv / ST) & 1);
+                    for (int t = 0; t < nt && ok; ++t) {
+                        for (int half = 0; half < 2 && ok; ++half) {
+                            ok = wait(p_full + 16 * half + 8 * t, j & 1);
+                            if (!ok) break;
+                            tc_after();
+                            values(t, iv % ST, half, j > 0 || half > 0);
+                        }
+                        if (!ok) break;
+                        if (!more) done(o_full + 8 * t);
+                        if (t == nt - 1) done(empty + 8 * (iv % ST));
+                        if (more) {
+                            if (t == 0) ok = wait(full + 8 * (ik % ST), (ik / ST) & 1);
+                            if (!ok) break;
+                            scores(t, ik % ST);
+                        }
+                    }
+                    if (ok && more) done(empty + 8 * (ik % ST));
+                }
+            } else {
+                // The next tile's scores are taken while this one's softmax runs.
+                for (int j = 0; j < tiles && ok; ++j) {
+                    const int iv = 2 * j + 1, ik = iv + 1, t = j & 1;
+                    if (j + 1 < tiles) {
+                        ok = wait(full + 8 * (ik % ST), (ik / ST) & 1);
+                        if (!ok) break;
+                        tc_after();
+                        scores(1 - t, ik % ST);
+                        done(empty + 8 * (ik % ST));
+                    }
+                    ok = wait(full + 8 * (iv % ST), (iv / ST) & 1);
                     for (int half = 0; half < 2 && ok; ++half) {
-                        ok = wait(p_full + 16 * half + 8 * t, j & 1);
+                        ok = wait(p_full + 16 * half + 8 * t, (j >> 1) & 1);
                         if (!ok) break;
                         tc_after();
                         values(t, iv % ST, half, j > 0 || half > 0);
                     }
                     if (!ok) break;
-                    if (!more) done(o_full + 8 * t);
-                    if (t == nt - 1) done(empty + 8 * (iv % ST));
-                    if (more) {
-                        if (t == 0) ok = wait(full + 8 * (ik % ST), (ik / ST) & 1);
-                        if (!ok) break;
-                        scores(t, ik % ST);
-                    }
+                    done(empty + 8 * (iv % ST));
+                    done(o_full + 8 * t);
                 }
-                if (ok && more) done(empty + 8 * (ik % ST));
             }
             // Nothing is on its way in tensor memory when it is freed.
             done(drain);
@@ -480,7 +521,7 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
         if (!chunk_load<D, FMT, FULL>(a.c, table, a.w.table_pages, h, begin, end, ring, full, empty)) atomicOr(fault, kFaultTimeout);
     } else {
         regs_up<kRegsSoftmax>();
-        {   // Q, by both row tiles' warps
+        {   // Q, by all these warps
             constexpr int PIECES = D / 8, ROWS = 256 / PIECES;
             const int piece = threadIdx.x % PIECES, at_row = threadIdx.x / PIECES;
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(h) * G * a.q_head + piece * 8;
@@ -488,10 +529,10 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
             const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // the softmax uses |scale|
             const bool vec = flip == 0 && ((reinterpret_cast<uintptr_t>(q) & 15) | (a.q_tok & 7) | (a.q_head & 7)) == 0;
 #pragma unroll 4
-            for (int row = at_row; row < kChunkRows; row += ROWS) {
+            for (int row = at_row; row < S::ROWS; row += ROWS) {
                 const unsigned qr = min(r0 + row, nrows - 1), tok = qr / static_cast<unsigned>(G), g1 = qr - tok * G;
                 const bool there = wide && r0 + row < nrows;
-                const uint32_t to = q_s + (row >> 7) * S::TILE + tile_at(row & 127, piece);
+                const uint32_t to = q_s + (row >> 7) * S::QTILE + tile_at<128>(row & 127, piece);
                 const __nv_bfloat16* from = q + (sp.first + tok) * a.q_tok + g1 * a.q_head;
                 if (vec) {
                     cp_async16_to(to, there ? from : static_cast<const __nv_bfloat16*>(a.q), there ? 16 : 0);
@@ -512,7 +553,7 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
         const int t = warp >> 2;
         const int qr = r0 + threadIdx.x;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + 128 * t;
+        const uint32_t o_at = tmem + lanes + 256 + 128 * t;
         // Tokens before `mine` are seen by this thread's row (a row that is not there: all).
         const int mine = a.causal && qr < nrows ? min(end, sp.pos0 + qr / G + 1) : end;
         // No smaller than the least normal number: -inf times it stays -inf, and 2^(x 1e-38) is 1.
@@ -523,34 +564,44 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
         if (t == 0 || two) {
             int page = chunk_page(a.c, table, a.w.table_pages, begin, end, lane);
             for (int j = 0; j < tiles; ++j) {
-                const int at = begin + j * kChunkKeys;
-                const uint32_t live = __ballot_sync(0xffffffffu, page >= 0);
-                page = chunk_page(a.c, table, a.w.table_pages, at + kChunkKeys, end, lane);
-                ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * t, j & 1));
+                const int at = begin + j * KEYS;
+                const uint32_t live = __ballot_sync(0xffffffffu, page >= 0) & ALL;
+                const int buf = S::PAIR ? t : j & 1, phase = S::PAIR ? j & 1 : (j >> 1) & 1;
+                const uint32_t s_at = tmem + lanes + 128 * buf;
+                page = chunk_page(a.c, table, a.w.table_pages, at + KEYS, end, lane);
+                ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * buf, phase));
+                // Of one row tile: product j reports to barrier j & 1.  Waiting for product j - 2 here keeps the phases
+                // apart: the next one of that barrier, product j, cannot be before this iteration's weights.
+                if (!S::PAIR && j >= 2) ok = __all_sync(0xffffffffu, ok && mbar_wait(o_full + 8 * (j & 1), ((j - 2) >> 1) & 1));
                 if (!ok) break;
                 tc_after();
-                float s[kChunkKeys];
+                float s[KEYS];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
+                for (int i = 0; i < KEYS / 32; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
                 tmem_ld_wait();
                 const int lim = mine - at;
-                if (!__all_sync(0xffffffffu, lim >= kChunkKeys) || live != 0xff) {
+                if (!__all_sync(0xffffffffu, lim >= KEYS) || live != ALL) {
 #pragma unroll
-                    for (int i = 0; i < kChunkKeys; ++i)
+                    for (int i = 0; i < KEYS; ++i)
                         if (i >= lim || !((live >> (i >> 4)) & 1)) s[i] = -INFINITY;
                 }
                 float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int i = 4; i < kChunkKeys; i += 8)
+                for (int i = 4; i < KEYS; i += 8)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        top[k] = i + 4 + k < kChunkKeys ? fmaxf(fmaxf(top[k], s[i + k]), s[i + 4 + k]) : fmaxf(top[k], s[i + k]);
+                        top[k] = i + 4 + k < KEYS ? fmaxf(fmaxf(top[k], s[i + k]), s[i + 4 + k]) : fmaxf(top[k], s[i + k]);
                 const float peak = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * log2s);
                 if (__any_sync(0xffffffffu, peak > m + 8.0f)) {
                     const float f = exp2_fast(m - (peak == -INFINITY ? 0.0f : peak));
                     l *= f;
                     m = peak;
-                    if (j > 0) {   // the product before is done: this tile's scores came after it
+                    if (j > 0) {
+                        if (!S::PAIR) {   // of a pair, the product before is done: this tile's scores came after it
+                            ok = __all_sync(0xffffffffu, mbar_wait(o_full + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1));
+                            if (!ok) break;
+                            tc_after();
+                        }
 #pragma unroll
                         for (int i = 0; i < D; i += 16) {
                             float o[16];
@@ -566,7 +617,7 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                 const uint64_t low2 = pack2(low, low);
                 uint64_t sum[2] = {pack2(l, 0.0f), pack2(0.0f, 0.0f)};
 #pragma unroll
-                for (int part = 0; part < 4; ++part) {
+                for (int part = 0; part < KEYS / 32; ++part) {
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -578,10 +629,10 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                         p[i] = bf16x2(x, y);
                     }
                     tmem_st16(s_at + 16 * part, p);
-                    if (part & 1) {
+                    if (KEYS == 64 || (part & 1)) {   // half of the tile
                         tmem_st_wait();
                         tc_before();
-                        mbar_arrive(p_full + 8 * (part - 1) + 8 * t);
+                        mbar_arrive(p_full + 16 * (KEYS == 64 ? part : part >> 1) + 8 * buf);
                     }
                 }
                 float l0, l1;
@@ -589,7 +640,8 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                 l = l0 + l1;
             }
             if (ok && tiles > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait(o_full + 8 * t, 0));
+                const int last = tiles - 1;
+                ok = __all_sync(0xffffffffu, S::PAIR ? mbar_wait(o_full + 8 * t, 0) : mbar_wait(o_full + 8 * (last & 1), (last >> 1) & 1));
                 tc_after();
             }
             if (!ok) {

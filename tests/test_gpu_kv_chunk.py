@@ -35,6 +35,11 @@ def both(fathom, cache, fmt, q, table, cu, length, new, most, causal=True, scale
     (1, 3, 64, 32, [(200, 3001)]),
     (1, 5, 128, 256, [(260, 1500), (1, 900), (0, 10)]),
     (3, 7, 64, 64, [(19, 700), (100, 101)]),
+    (1, 1, 256, 64, [(128, 128), (129, 129), (64, 64)]),   # beyond 128 channels: one row tile, 64 tokens
+    (1, 4, 256, 16, [(33, 65), (32, 63), (16, 3000)]),
+    (2, 2, 160, 32, [(70, 1000), (0, 5)]),
+    (1, 8, 224, 256, [(40, 777)]),
+    (1, 3, 192, 128, [(50, 320), (300, 301)]),
 ])
 def test_edges_of_tiles(fathom_gpu, fmt, causal, H, G, D, page, lens):
     lens = [(min(n, t), t) for n, t in lens]
@@ -64,7 +69,7 @@ def test_widths_between(fathom_gpu, fmt, causal, layout, H, G, D, page, lens):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "int8"])
-@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_maximum_that_keeps_growing(fathom_gpu, fmt, D):
     """Keys that point at the queries more and more along the sequence, by steps smaller and larger than the 2^8 below
     which the running maximum stays; then the other way round."""
@@ -155,3 +160,26 @@ def test_blocks_of_very_different_sizes(fathom_gpu, fmt, dtype, span, D, new):
     fathom_gpu.kv_write(cache, k.contiguous(), v.contiguous(), table, cu_all, length)
     q = (queries((new, 4, D // 32, 32), 3, torch.float32) / chan).flatten(2).to(TYPES[dtype])
     both(fathom_gpu, cache, fmt, q, table, cu, length, new, n)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("D", [32, 64, 128, 160, 256])
+def test_again_and_again(fathom_gpu, fmt, D):
+    """Many calls one behind another, over maxima that grow often (products and softmax meet in every order): the same
+    result each time, and no wait that ran out."""
+    lens = [(256, 8000), (100, 4000)]
+    pages, table, cu, length = make_batch(lens, 64)
+    cache = make_cache(fathom_gpu, fmt, pages, 4, D, 64)
+    k = torch.randn(12000, 4, D, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    k *= torch.cat([torch.linspace(0.1, 12, 8000), torch.linspace(0.1, 12, 4000)]).to(DEV)[:, None, None]
+    v = torch.randn(12000, 4, D, generator=torch.Generator(device=DEV).manual_seed(2), device=DEV)
+    fathom_gpu.kv_write(cache, k, v, table, torch.tensor([0, 8000, 12000], dtype=torch.int32, device=DEV), length)
+    q = queries((356, 16, D), 4)
+    want = fathom_gpu.paged_attention(cache, q, table, cu, length, 256, 8000)
+    got = [fathom_gpu.paged_attention(cache, q, table, cu, length, 256, 8000) for _ in range(40)]
+    assert fathom_gpu.device_status() == fathom_gpu.OK
+    assert all(torch.equal(g, want) for g in got)
+    few = torch.tensor([0, 100, 255, 256, 300, 355])
+    ref = okv.attend(host(cache), fmt, q.float().cpu().numpy(), table.cpu().numpy(), cu.cpu().numpy(), length.cpu().numpy(),
+                     D ** -0.5)
+    check_attention(want[few], tuple(x[few.numpy()] for x in ref), 8000, D, torch.bfloat16)
