@@ -594,7 +594,7 @@ int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, voi
  *   max_len         cached tokens of a sequence that are read at most.
  *                   Both size the launch: give the batch's largest, or a bound
  *                   that holds for every replay of a captured graph.
- *   scale           usually 1/sqrt(D); finite.
+ *   scale           usually 1/sqrt(D); at most 1e38 in magnitude.
  *   out             DEVICE out, [rows][H][G][D], of q's type.
  *   workspace, ws_bytes  DEVICE scratch of at least
  *                   fathom_paged_attention_workspace_bytes() bytes for the
@@ -603,12 +603,18 @@ int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, voi
  *                   call's work is done: calls that may overlap on the GPU
  *                   need one each.
  * Arithmetic: products of bf16 values summed in fp32, the softmax in fp32.
- * fp32 queries are taken as the sum of three bf16 parts (all 24 bits); the
- * weights exp(s - max) enter the value product in bf16 for bf16 queries of
- * prompt chunks, in two bf16 parts (16 bits) for bf16 queries otherwise, and in three for
- * fp32 queries.  Cached values of tokens below length should be finite where
- * rows that do not see them are to stay finite; what lies beyond length in
- * a page is never used.  1 <= G <= 8.
+ * fp32 queries are taken as the sum of three bf16 parts (all 24 bits), and so
+ * are the weights exp(s - max) that enter the value product; with bf16 queries
+ * they enter it in bf16 (half a step, 2^-9 of a weight) and their sum is of the
+ * unrounded ones.  The result does not depend on timing.
+ * Cached values of tokens below length should be finite where rows that do not
+ * see them are to stay finite; what lies beyond length in a page is never
+ * used.  A row that sees a NaN is NaN.  E4M3 codes that are NaN (0x7f, 0xff;
+ * never written by fathom_kv_write) must not be in the cache.
+ * 1 <= G <= 8; max_len <= 2^30; min(max_new, rows)*G < 2^31 (ERR_UNSUPPORTED
+ * beyond).  bf16 queries of more than 32 rows*G run on a kernel with bounded
+ * waits between its warps: should one run out, which takes a fault, the call's
+ * output is void and fathom_device_status() returns FATHOM_ERR_TIMEOUT.
  */
 size_t fathom_paged_attention_workspace_bytes(int H, int G, int D, int64_t rows, int B, int64_t max_new,
                                               int64_t max_len, int q_dtype);

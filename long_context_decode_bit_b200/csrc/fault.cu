@@ -1,7 +1,8 @@
 // Device fault word: set by a kernel whose bounded wait gave up (bit 0), or,
 // in the debug build, whose bounds check failed (bit 1).
 //
-// The scan's shared-memory ring waits on mbarriers with a poll limit.  A wait
+// The scan's shared-memory ring, and the warps of the paged attention's chunk
+// kernel, wait on mbarriers with a poll limit.  A wait
 // that runs out (which a correct launch never does) makes the kernel set
 // this word and leave its loop instead of spinning for ever; the scores of
 // that launch are then void.  The union kernel turns a set word into

@@ -17,12 +17,15 @@ int64_t round_up(int64_t x, int64_t to) { return ceil_div(x, to) * to; }
 // time of `start` of them to begin and end a CTA), and writing and joining the
 // stretches' sums.  A batch's longest sequence is `longest` of the `items`;
 // the others are taken to be half as long, since only the device knows.
+// From eight waves of CTAs on there is nothing to gain, and with longer bounds
+// than the sequences have the parts would only take memory.
 // Returns the tiles of a stretch.
 int64_t cut(int64_t tiles, int64_t items, int64_t longest, int64_t heads, int D, int64_t at_once, double us, int64_t start)
 {
     double best = 0.0;
     int64_t each = tiles;
-    for (int64_t n = 1; n <= 32 && n <= tiles; ++n) {
+    const int64_t most = std::min({int64_t{32}, tiles, ceil_div(8 * at_once, items)});
+    for (int64_t n = 1; n <= most; ++n) {
         const int64_t len = ceil_div(tiles, n);
         const int64_t waves = ceil_div(longest * n + (items - longest) * ceil_div(n, 2), at_once);
         const double cost = waves * (len + start) * us + (n > 1 ? 4.0 + static_cast<double>(n) * heads * D * 8 / 5e6 : 0.0);

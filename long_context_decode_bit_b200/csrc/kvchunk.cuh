@@ -30,6 +30,8 @@
 // sets the fault word and leaves its loop, and the CTA frees its tensor memory.
 #pragma once
 
+#include <atomic>
+
 #include "kvrows.cuh"
 #include "ring.cuh"
 
@@ -704,11 +706,14 @@ int launch_chunk_t(const KvRowsArgs& g, cudaStream_t stream)
     using S = ChunkShape<D, FMT>;
     const void* f = reinterpret_cast<const void*>(kv_chunk_kernel<D, FMT, FULL>);
     // The roles' registers must add up to no more than the block is launched with, or the softmax waits for ever.
-    static const int launch_regs = [f] {
+    static std::atomic<int> launch_regs{0};   // the same on every device
+    if (launch_regs.load(std::memory_order_relaxed) == 0) {
         cudaFuncAttributes attr;
-        return cudaFuncGetAttributes(&attr, f) == cudaSuccess ? attr.numRegs : 0;
-    }();
-    if (4 * launch_regs < 2 * kRegsSoftmax + kRegsLoad + kRegsIssue) return FATHOM_ERR_UNSUPPORTED;
+        const cudaError_t e = cudaFuncGetAttributes(&attr, f);
+        if (e != cudaSuccess) return cuda_status(e);
+        launch_regs.store(attr.numRegs, std::memory_order_relaxed);
+    }
+    if (4 * launch_regs.load(std::memory_order_relaxed) < 2 * kRegsSoftmax + kRegsLoad + kRegsIssue) return FATHOM_ERR_UNSUPPORTED;
     int32_t* fault = nullptr;
     int st = device_fault_word(&fault);
     if (st) return st;

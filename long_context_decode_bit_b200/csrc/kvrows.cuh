@@ -114,6 +114,7 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttend& a, int b)
     s.first = a.w.cu[b];
     const int64_t end = a.w.cu[b + 1], len = a.w.length[b];
     s.rows = static_cast<int32_t>(max(int64_t{0}, min(min(end, static_cast<int64_t>(a.w.rows)) - s.first, a.max_new)));
+    if (s.first < 0) s.rows = 0;   // no such rows
     s.pos0 = static_cast<int32_t>(len - end + s.first);
     s.keys = static_cast<int32_t>(max(int64_t{0}, min(len, a.max_len)));
     return s;

@@ -1,5 +1,9 @@
 """Attention of prompt chunks over the paged cache against the 64-bit oracle, at the places where its tiles (256 query
 rows, 128 tokens), its ring of tiles and its stretches of tokens begin and end."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -183,3 +187,35 @@ def test_again_and_again(fathom_gpu, fmt, D):
     ref = okv.attend(host(cache), fmt, q.float().cpu().numpy(), table.cpu().numpy(), cu.cpu().numpy(), length.cpu().numpy(),
                      D ** -0.5)
     check_attention(want[few], tuple(x[few.numpy()] for x in ref), 8000, D, torch.bfloat16)
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_first_call_under_capture(new):
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, os.path.join(here, "_capture_child.py"), str(new)], cwd=os.path.dirname(here),
+                       env=dict(os.environ, PYTHONPATH=os.path.dirname(here)), capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("new", [2, 100])
+def test_row_bounds_that_make_no_sense(fathom_gpu, new):
+    """Offsets below zero, beyond the rows, or decreasing: no row outside the call's is read or written, and sequences
+    whose own bounds are sound get their results."""
+    lens = [(new, 300)] * 4
+    pages, table, cu, length = make_batch(lens, 64)
+    cache = make_cache(fathom_gpu, "int8", pages, 2, 128, 64)
+    fill(fathom_gpu, cache, lens, table)
+    for dt in TYPES.values():
+        q = queries((4 * new + 64, 8, 128), 4, dt)
+        mid = q[32:-32]
+        good = fathom_gpu.paged_attention(cache, mid, table, cu, length, new, 300)
+        for bad in ([-5, new, 2 * new, 3 * new, 4 * new], [0, new, 2 * new, 1 << 30, 4 * new], [0, new, 2 * new, new, 0],
+                    [1 << 30, new, 2 * new, 3 * new, 7 * new], [-(1 << 31), new, 2 * new, -7, (1 << 31) - 1]):
+            c = torch.tensor(bad, dtype=torch.int32, device=DEV)
+            out = torch.full((4 * new + 64, 8, 128), 7.0, dtype=dt, device=DEV)
+            fathom_gpu.paged_attention(cache, mid, table, c, length, new, 300, out=out[32:-32])
+            assert torch.equal(out[32 + new:32 + 2 * new], good[new:2 * new])
+            assert (out[:32] == 7.0).all() and (out[-32:] == 7.0).all()
+            kv = [torch.full((2, 4 * new + 64, 128), 7.0, device=DEV) for _ in range(2)]
+            fathom_gpu.kv_read(cache, table, c, length, 4 * new, out=[t[:, 32:-32] for t in kv])
+            assert all((t[:, :32] == 7.0).all() and (t[:, -32:] == 7.0).all() for t in kv)

@@ -159,3 +159,17 @@ def test_binding_checks():
         fathom.kv_read(c, table, cu, length, 3, out=(None, None))
     with pytest.raises(ValueError):
         fathom.paged_union_attention(c, torch.zeros(2, 2, 64).bfloat16(), table, 3, cu[None], length)
+
+
+def test_largest_sizes(lib):
+    """Sizes beyond what a token or a row of queries may be counted to."""
+    def attend(rows_=10, max_new=5, max_len=256, G=4, scale=0.1):
+        return lib.fathom_paged_attention(cache(), rows(rows=rows_), FAKE, 1, 4096, 128, G, max_new, max_len, 1, scale, FAKE + 2,
+                                          FAKE + 1, 1 << 62, None)
+    assert attend(max_len=(1 << 30) + 1) == fathom.ERR_UNSUPPORTED
+    assert attend(rows_=(1 << 28) + 1, max_new=1 << 30, G=8) == fathom.ERR_UNSUPPORTED
+    assert attend(scale=1.1e38) == fathom.ERR_INVALID_ARG and attend(scale=-1.1e38) == fathom.ERR_INVALID_ARG
+    ws = lib.fathom_paged_attention_workspace_bytes
+    for max_len in (1, 1 << 30):   # a bound that covers any replay of a graph asks for no unbounded scratch
+        for new in (1, 2, 40, 5000):
+            assert ws(8, 4, 128, new, 1, new, max_len, 1) <= 160 * 592 * 8 * 4 * 136
