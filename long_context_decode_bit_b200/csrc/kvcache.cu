@@ -83,14 +83,25 @@ __device__ __forceinline__ void kv_values(const Raw16<DT>& raw, float (&x)[16])
     }
 }
 
-// Codes of 16 channels and their block's exponent byte.  Both threads of the block take part.
-template <int FMT>
-__device__ __forceinline__ uint4 kv_encode16(const float (&x)[16], uint32_t* byte)
+// Bit pattern (fp32) of the largest magnitude of a 32-channel block, of which this thread and its neighbour have half each.
+template <int DT>
+__device__ __forceinline__ uint32_t kv_largest(const Raw16<DT>& raw)
 {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    for (int i = 0; i < (DT == FATHOM_KEYS_BF16 ? 2 : 4); ++i) {
+        const uint32_t w[4] = {raw.u[i].x, raw.u[i].y, raw.u[i].z, raw.u[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = DT == FATHOM_KEYS_BF16 ? __vmaxu2(m, w[j] & 0x7fff7fffu) : max(m, w[j] & 0x7fffffffu);
+    }
+    if (DT == FATHOM_KEYS_BF16) m = max(m << 16, m & 0xffff0000u);
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+}
+
+// Codes of 16 channels and their block's exponent byte, m from kv_largest.
+template <int FMT>
+__device__ __forceinline__ uint4 kv_encode16(float (&x)[16], uint32_t m, uint32_t* byte)
+{
     if (m >= 0x7f800000u) {
         *byte = 255;
         return make_uint4(0, 0, 0, 0);
@@ -103,7 +114,10 @@ __device__ __forceinline__ uint4 kv_encode16(const float (&x)[16], uint32_t* byt
     *byte = static_cast<uint32_t>(e + 127);
     const float f = kv_pow2(static_cast<uint32_t>(127 - e));
     uint32_t w[4];
-    const float most = FMT == FATHOM_KV_INT8 && e == 121 ? 127.0f / f : INFINITY;   // only there a code could become 128
+    if (FMT == FATHOM_KV_INT8 && e == 121) {   // only there a code could become 128
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -0x7fp121f), 0x7fp121f);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (FMT == FATHOM_KV_INT8) {
@@ -111,7 +125,7 @@ __device__ __forceinline__ uint4 kv_encode16(const float (&x)[16], uint32_t* byt
             uint32_t r[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                r[j] = __float_as_uint(fmaf(fminf(fmaxf(x[4 * i + j], -most), most), f, 12582912.0f));
+                r[j] = __float_as_uint(fmaf(x[4 * i + j], f, 12582912.0f));
             w[i] = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
         } else {
             const float2 lo = make_float2(x[4 * i] * f, x[4 * i + 1] * f), hi = make_float2(x[4 * i + 2] * f, x[4 * i + 3] * f);
@@ -197,7 +211,7 @@ kv_write_kernel(const KvCache c, const KvRows w, const void* __restrict__ k, con
                 }
             } else {
                 uint32_t byte;
-                const uint4 codes = kv_encode16<FMT>(y, &byte);
+                const uint4 codes = kv_encode16<FMT>(y, kv_largest<DT>(x[i][s]), &byte);
                 if (live) {
                     *reinterpret_cast<uint4*>(data + to + j) = codes;
                     unsigned char* sc = const_cast<unsigned char*>(s ? c.vs : c.ks);
