@@ -574,7 +574,7 @@ int fathom_kv_write(const fathom_kv_cache* cache, const fathom_kv_rows* rows, co
  * out[h*stride_h + r*stride_tok + j], fp32 or bf16 (exact in both), the
  * layout that fathom_pack, fathom_calibrate and fathom_union_attention take.
  *
- *   out_k, out_v    DEVICE out; either may be NULL.
+ *   out_k, out_v    DEVICE out, apart from one another; either may be NULL.
  */
 int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, void* out_k, void* out_v, int dtype,
                    int64_t stride_h, int64_t stride_tok, fathom_stream_t stream);

@@ -186,6 +186,7 @@ int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, voi
     FATHOM_TRY(check_cache(cache, &c));
     FATHOM_TRY(check_row_ptrs(rows, &w));
     FATHOM_TRY(check_all_here(out_k ? out_k : out_v, out_v ? out_v : out_k));
+    if (out_k == out_v) return FATHOM_ERR_INVALID_ARG;
     return launch_kv_read(c, cache->format, w, out_k, out_v, dtype, stride_h, stride_tok,
                           reinterpret_cast<cudaStream_t>(stream));
 }

@@ -1,7 +1,7 @@
 // Attention of few query rows over rows of the paged cache, on the matrix
 // units a warp drives by itself (mma.sync, m16n8k16): single tokens, the
 // union of the scan's winners, and what kvchunk.cuh does not take (fp32
-// queries, more than 128 channels).
+// queries, and up to 32 rows of bf16 ones).
 //
 // The work is bound by reading K and V, so the products are turned round to
 // have the cached rows as the 16-row operand and the (few) query rows as the

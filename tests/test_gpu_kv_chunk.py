@@ -219,3 +219,11 @@ def test_row_bounds_that_make_no_sense(fathom_gpu, new):
             kv = [torch.full((2, 4 * new + 64, 128), 7.0, device=DEV) for _ in range(2)]
             fathom_gpu.kv_read(cache, table, c, length, 4 * new, out=[t[:, 32:-32] for t in kv])
             assert all((t[:, :32] == 7.0).all() and (t[:, -32:] == 7.0).all() for t in kv)
+
+
+def test_one_place_for_two_outputs(fathom_gpu):
+    pages, table, cu, length = make_batch([(5, 30)], 16)
+    cache = make_cache(fathom_gpu, "int8", pages, 1, 64, 16)
+    out = torch.zeros(1, 5, 64, device=DEV)
+    with pytest.raises(fathom_gpu.FathomError):
+        fathom_gpu.kv_read(cache, table, cu, length, 5, out=(out, out))

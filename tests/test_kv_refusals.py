@@ -173,3 +173,9 @@ def test_largest_sizes(lib):
     for max_len in (1, 1 << 30):   # a bound that covers any replay of a graph asks for no unbounded scratch
         for new in (1, 2, 40, 5000):
             assert ws(8, 4, 128, new, 1, new, max_len, 1) <= 160 * 592 * 8 * 4 * 136
+
+
+def test_workspace_that_is_not_what_it_says():
+    wide = torch.zeros(1, dtype=torch.uint8).expand(1 << 20)   # one byte that calls itself a mebibyte
+    with pytest.raises(ValueError, match="contiguous"):
+        fathom._workspace(wide, 1 << 20, wide, None)
