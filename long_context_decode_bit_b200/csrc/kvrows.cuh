@@ -186,7 +186,8 @@ struct RowsShape {
     static constexpr int NB = D / kKvBlock, SBW = NB <= 4 ? 4 : 8;                 // exponent bytes of a row, and their place
     static constexpr int LPR = PP % 4 == 0 ? 4 : 2, RPL = LPR / 2;                 // lanes that copy a row, rows of a lane
     static constexpr int STAGE = 32 * RB + (CODED ? 32 * SBW : 0);                 // 16 rows of K and of V
-    static constexpr int STAGES = STAGE <= 2304 ? 5 : 3;
+    // Of wide tiles and three parts of Q, two: two CTAs fit an SM (128 channels of bf16, fp32 queries: 78 -> 63 us).
+    static constexpr int STAGES = STAGE <= 2304 ? 5 : (!CODED && WIDEQ && NT > 1 && STAGE >= 8192 ? 2 : 3);
     static constexpr int RING = kRowsWarps * STAGES * STAGE;
     static constexpr int QB = static_cast<int>(sizeof(uint2)) * NQ * KS * NT * 32; // Q's operand registers
     static constexpr int OB = static_cast<int>(sizeof(float)) * NT * 8 * (D + 8);  // value sums, where the ring was
