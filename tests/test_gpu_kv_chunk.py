@@ -227,3 +227,25 @@ def test_one_place_for_two_outputs(fathom_gpu):
     out = torch.zeros(1, 5, 64, device=DEV)
     with pytest.raises(fathom_gpu.FathomError):
         fathom_gpu.kv_read(cache, table, cu, length, 5, out=(out, out))
+
+
+@pytest.mark.parametrize("fmt,D", [("bf16", 128), ("int8", 64), ("int8", 256)])
+def test_two_chunks_at_once(fathom_gpu, fmt, D):
+    """Two calls on two streams, many times over, each with scratch of its own: the results of one call alone."""
+    lens = [(300, 5000), (150, 2500)]
+    pages, table, cu, length = make_batch(lens, 32)
+    cache = make_cache(fathom_gpu, fmt, pages, 2, D, 32)
+    fill(fathom_gpu, cache, lens, table)
+    qs = [queries((450, 8, D), 4 + i) for i in range(2)]
+    want = [fathom_gpu.paged_attention(cache, q, table, cu, length, 300, 5000) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(fathom_gpu.paged_attention(cache, qs[i], table, cu, length, 300, 5000))
+            got[i].append(fathom_gpu.paged_attention(cache, qs[i], table, cu, length, 300, 5000, stream=s))   # named instead
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i]) for i in range(2) for x in got[i])
+    assert fathom_gpu.device_status() == fathom_gpu.OK
