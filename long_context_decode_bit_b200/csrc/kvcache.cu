@@ -1,18 +1,20 @@
 // fathom_kv_write and fathom_kv_read: rows into the paged cache and back.
 //
-// A thread takes 16 channels of a few consecutive rows of K and of V; the two
-// threads of a 32-channel block find its largest magnitude with a shuffle.
-// Magnitudes are compared as bit patterns, which orders NaN above infinity
-// above every number, so one compare finds the blocks that cannot be kept.
-// The exponent comes from the pattern too (exponent field, and one compare of
-// the fraction with the value that would round over the largest code), so no
-// division or logarithm is rounded anywhere and x 2^-e is exact before the one
-// rounding to the code.
+// A thread takes 16 channels of one row of K and of V; the two threads of a
+// 32-channel block find its largest magnitude with a shuffle.  Magnitudes are
+// compared as bit patterns, which orders NaN above infinity above every
+// number, so one compare finds the blocks that cannot be kept.  The exponent
+// comes from the pattern too (exponent field, and one compare of the fraction
+// with the value that would round over the largest code), so no division or
+// logarithm is rounded anywhere and x 2^-e is exact before the one rounding to
+// the code.
 //
 // Both kernels stream: bound by HBM, or by the launch when a decode step
 // writes one token.  A row's place is three loads that wait for one another
-// (its sequence, its length, its page): with several rows to a thread their
-// chains and the copies behind them run side by side.
+// (its sequence, its length, its page); many small threads hide the chain
+// better than several rows to a thread (a 128k int8 session of 8 groups read
+// back in bf16: 130 us, 6.3 TB/s, against 137 us with four; 32k tokens written and
+// read back 67 us against 80; a token 4.4 us against 6.6).
 #include "kv.cuh"
 
 namespace fathom {
@@ -20,7 +22,6 @@ namespace fathom {
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr int64_t kKvOneEach = 148 * 1024;   // threads that are one wave
 
 __device__ __forceinline__ void ld_global32(const void* p, uint4* u)
 {
@@ -170,53 +171,44 @@ __device__ __forceinline__ int kv_place(const KvCache& c, const KvRows& w, int r
     return kv_page(c, w.table + b * w.table_stride, w.table_pages, pos);
 }
 
-template <int FMT, int DT, int VEC, int N>
+template <int FMT, int DT, int VEC>
 __global__ void __launch_bounds__(kKvThreads)
 kv_write_kernel(const KvCache c, const KvRows w, const void* __restrict__ k, const void* __restrict__ v,
                 int64_t stride_tok, int64_t stride_h)
 {
     const int per = c.D >> 4, units = c.H * per;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x;
-    const int64_t first = t / units;
-    const int unit = static_cast<int>(t - first * units), h = unit / per, j = (unit - h * per) << 4;
-    int page[N], token[N];
-    Raw16<DT> x[N][2];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int64_t row = first * N + i;
-        page[i] = row < w.rows ? kv_place(c, w, static_cast<int>(row), &token[i]) : -2;
-        x[i][0] = x[i][1] = {};
-        if (page[i] >= 0) {   // the same for both threads of a block
-            const int64_t at = row * stride_tok + h * stride_h + j;
-            kv_load16<DT, VEC>(k, at, &x[i][0]);
-            kv_load16<DT, VEC>(v, at, &x[i][1]);
-        }
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x, row = t / units;
+    const int unit = static_cast<int>(t - row * units), h = unit / per, j = (unit - h * per) << 4;
+    int token = 0;
+    const int page = row < w.rows ? kv_place(c, w, static_cast<int>(row), &token) : -2;
+    const bool live = page >= 0;   // the same for both threads of a block
+    Raw16<DT> x[2] = {};
+    if (live) {
+        const int64_t at = row * stride_tok + h * stride_h + j;
+        kv_load16<DT, VEC>(k, at, &x[0]);
+        kv_load16<DT, VEC>(v, at, &x[1]);
     }
+    const int64_t to = live ? kv_off(c, page, h, token) : 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const bool live = page[i] >= 0;
-        const int64_t to = live ? kv_off(c, page[i], h, token[i]) : 0;
+    for (int s = 0; s < 2; ++s) {
+        unsigned char* data = const_cast<unsigned char*>(s ? c.v : c.k);
+        float y[16];
+        kv_values<DT>(x[s], y);
+        if (FMT == FATHOM_KV_BF16) {
+            if (live) {
+                uint4* o = reinterpret_cast<uint4*>(data + to + 2 * j);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            unsigned char* data = const_cast<unsigned char*>(s ? c.v : c.k);
-            float y[16];
-            kv_values<DT>(x[i][s], y);
-            if (FMT == FATHOM_KV_BF16) {
-                if (live) {
-                    uint4* o = reinterpret_cast<uint4*>(data + to + 2 * j);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        o[q] = make_uint4(bf16x2(y[8 * q], y[8 * q + 1]), bf16x2(y[8 * q + 2], y[8 * q + 3]),
-                                          bf16x2(y[8 * q + 4], y[8 * q + 5]), bf16x2(y[8 * q + 6], y[8 * q + 7]));
-                }
-            } else {
-                uint32_t byte;
-                const uint4 codes = kv_encode16<FMT>(y, kv_largest<DT>(x[i][s]), &byte);
-                if (live) {
-                    *reinterpret_cast<uint4*>(data + to + j) = codes;
-                    unsigned char* sc = const_cast<unsigned char*>(s ? c.vs : c.ks);
-                    if ((j & 31) == 0) sc[kv_scale_off(c, page[i], h, token[i]) + (j >> 5)] = static_cast<unsigned char>(byte);
-                }
+                for (int q = 0; q < 2; ++q)
+                    o[q] = make_uint4(bf16x2(y[8 * q], y[8 * q + 1]), bf16x2(y[8 * q + 2], y[8 * q + 3]),
+                                      bf16x2(y[8 * q + 4], y[8 * q + 5]), bf16x2(y[8 * q + 6], y[8 * q + 7]));
+            }
+        } else {
+            uint32_t byte;
+            const uint4 codes = kv_encode16<FMT>(y, kv_largest<DT>(x[s]), &byte);
+            if (live) {
+                *reinterpret_cast<uint4*>(data + to + j) = codes;
+                unsigned char* sc = const_cast<unsigned char*>(s ? c.vs : c.ks);
+                if ((j & 31) == 0) sc[kv_scale_off(c, page, h, token) + (j >> 5)] = static_cast<unsigned char>(byte);
             }
         }
     }
@@ -260,77 +252,56 @@ __device__ __forceinline__ void kv_store16(void* out, int64_t to, const uint32_t
     }
 }
 
-template <int FMT, int DT, int VEC, int N>
+template <int FMT, int DT, int VEC>
 __global__ void __launch_bounds__(kKvThreads)
 kv_read_kernel(const KvCache c, const KvRows w, void* out_k, void* out_v, int64_t stride_h, int64_t stride_tok)
 {
     constexpr int PIECES = FMT == FATHOM_KV_BF16 ? 2 : 1;
     const int per = c.D >> 4;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x;
-    const int64_t first = t / per;
-    const int j = static_cast<int>(t - first * per) << 4;
-    const int h = blockIdx.y;
-    int page[N], token[N];
-    uint4 raw[N][2][PIECES];
-    uint32_t byte[N][2];
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kKvThreads + threadIdx.x, row = t / per;
+    const int j = static_cast<int>(t - row * per) << 4, h = blockIdx.y;
+    if (row >= w.rows) return;
+    int token = 0;
+    const int page = kv_place(c, w, static_cast<int>(row), &token);
+    if (page == -2) return;   // not a row of any sequence
+    uint4 raw[2][PIECES] = {};
+    uint32_t byte[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int64_t row = first * N + i;
-        page[i] = row < w.rows ? kv_place(c, w, static_cast<int>(row), &token[i]) : -2;
+    for (int s = 0; s < 2; ++s) {
+        if (page >= 0 && (s ? out_v : out_k)) {
+            const uint4* from = reinterpret_cast<const uint4*>((s ? c.v : c.k) + kv_off(c, page, h, token) + j * kv_elem_bytes<FMT>());
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            byte[i][s] = 0;
-#pragma unroll
-            for (int q = 0; q < PIECES; ++q) raw[i][s][q] = make_uint4(0, 0, 0, 0);
-            if (page[i] >= 0 && (s ? out_v : out_k)) {
-                const uint4* from = reinterpret_cast<const uint4*>((s ? c.v : c.k) + kv_off(c, page[i], h, token[i]) + j * kv_elem_bytes<FMT>());
-#pragma unroll
-                for (int q = 0; q < PIECES; ++q) raw[i][s][q] = __ldg(from + q);
-                if (FMT != FATHOM_KV_BF16)
-                    byte[i][s] = __ldg((s ? c.vs : c.ks) + kv_scale_off(c, page[i], h, token[i]) + (j >> 5));
-            }
+            for (int q = 0; q < PIECES; ++q) raw[s][q] = __ldg(from + q);
+            if (FMT != FATHOM_KV_BF16) byte[s] = __ldg((s ? c.vs : c.ks) + kv_scale_off(c, page, h, token) + (j >> 5));
         }
     }
+    const int64_t to = h * stride_h + row * stride_tok + j;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (page[i] == -2) continue;   // not a row of any sequence
-        const int64_t to = h * stride_h + (first * N + i) * stride_tok + j;
+    for (int s = 0; s < 2; ++s) {
+        void* out = s ? out_v : out_k;
+        if (!out) continue;
+        uint32_t x[8];
+        if constexpr (FMT == FATHOM_KV_BF16) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            void* out = s ? out_v : out_k;
-            if (!out) continue;
-            uint32_t x[8];
-            if constexpr (FMT == FATHOM_KV_BF16) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    x[4 * q] = raw[i][s][q].x;
-                    x[4 * q + 1] = raw[i][s][q].y;
-                    x[4 * q + 2] = raw[i][s][q].z;
-                    x[4 * q + 3] = raw[i][s][q].w;
-                }
-            } else {
-                kv_decode16<FMT>(raw[i][s][0], byte[i][s], x);
+            for (int q = 0; q < 2; ++q) {
+                x[4 * q] = raw[s][q].x;
+                x[4 * q + 1] = raw[s][q].y;
+                x[4 * q + 2] = raw[s][q].z;
+                x[4 * q + 3] = raw[s][q].w;
             }
-            kv_store16<DT, VEC>(out, to, x);
+        } else {
+            kv_decode16<FMT>(raw[s][0], byte[s], x);
         }
+        kv_store16<DT, VEC>(out, to, x);
     }
 }
 
-// One row to a thread while that is a wave of threads at most (a token or a few: the chain of loads is the time);
-// beyond, four of bf16 or two of fp32.
 template <int FMT, int DT, int VEC>
 int launch_kv_write_v(const KvCache& c, const KvRows& w, const void* k, const void* v, int64_t stride_tok, int64_t stride_h,
                       cudaStream_t stream)
 {
-    constexpr int N = DT == FATHOM_KEYS_BF16 ? 4 : 2;
-    const int64_t units = static_cast<int64_t>(c.H) * (c.D / 16);
-    if (w.rows * units <= kKvOneEach) {
-        const unsigned grid = static_cast<unsigned>(ceil_div(w.rows * units, kKvThreads));
-        kv_write_kernel<FMT, DT, VEC, 1><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
-    } else {
-        const unsigned grid = static_cast<unsigned>(ceil_div(ceil_div(w.rows, N) * units, kKvThreads));
-        kv_write_kernel<FMT, DT, VEC, N><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
-    }
+    const unsigned grid = static_cast<unsigned>(ceil_div(static_cast<int64_t>(w.rows) * c.H * (c.D / 16), kKvThreads));
+    kv_write_kernel<FMT, DT, VEC><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
     return launch_status();
 }
 
@@ -338,15 +309,9 @@ template <int FMT, int DT, int VEC>
 int launch_kv_read_v(const KvCache& c, const KvRows& w, void* out_k, void* out_v, int64_t stride_h, int64_t stride_tok,
                      cudaStream_t stream)
 {
-    constexpr int N = DT == FATHOM_KEYS_BF16 ? 4 : 2;
-    const int64_t per = c.D / 16;
-    if (w.rows * per * c.H <= kKvOneEach) {
-        const dim3 grid(static_cast<unsigned>(ceil_div(w.rows * per, kKvThreads)), static_cast<unsigned>(c.H));
-        kv_read_kernel<FMT, DT, VEC, 1><<<grid, kKvThreads, 0, stream>>>(c, w, out_k, out_v, stride_h, stride_tok);
-    } else {
-        const dim3 grid(static_cast<unsigned>(ceil_div(ceil_div(w.rows, N) * per, kKvThreads)), static_cast<unsigned>(c.H));
-        kv_read_kernel<FMT, DT, VEC, N><<<grid, kKvThreads, 0, stream>>>(c, w, out_k, out_v, stride_h, stride_tok);
-    }
+    const dim3 grid(static_cast<unsigned>(ceil_div(static_cast<int64_t>(w.rows) * (c.D / 16), kKvThreads)),
+                    static_cast<unsigned>(c.H));
+    kv_read_kernel<FMT, DT, VEC><<<grid, kKvThreads, 0, stream>>>(c, w, out_k, out_v, stride_h, stride_tok);
     return launch_status();
 }
 

@@ -22,7 +22,9 @@
 // codes, but then powers have to be kept relative to a running largest and
 // weights below 2^-40 are lost; both took the same time.)  A dot product may
 // run over the channels in any order, so a lane takes consecutive bytes of a
-// row, and Q is laid out to match.
+// row, and Q is laid out to match.  fp32 queries and their weights are three
+// bf16 parts each (24 bits); the weights of bf16 queries are rounded to bf16,
+// 2^-9 of each, like the output they go into.
 #pragma once
 
 #include "kv.cuh"
@@ -187,7 +189,7 @@ struct RowsShape {
     static constexpr int LPR = PP % 4 == 0 ? 4 : 2, RPL = LPR / 2;                 // lanes that copy a row, rows of a lane
     static constexpr int STAGE = 32 * RB + (CODED ? 32 * SBW : 0);                 // 16 rows of K and of V
     // Of wide tiles and three parts of Q, two: two CTAs fit an SM (128 channels of bf16, fp32 queries: 78 -> 63 us).
-    static constexpr int STAGES = STAGE <= 2304 ? 5 : (!CODED && WIDEQ && NT > 1 && STAGE >= 8192 ? 2 : 3);
+    static constexpr int STAGES = !CODED && WIDEQ && NT > 1 && STAGE >= 8192 ? 2 : 3;
     static constexpr int RING = kRowsWarps * STAGES * STAGE;
     static constexpr int QB = static_cast<int>(sizeof(uint2)) * NQ * KS * NT * 32; // Q's operand registers
     static constexpr int OB = static_cast<int>(sizeof(float)) * NT * 8 * (D + 8);  // value sums, where the ring was
