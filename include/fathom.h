@@ -599,8 +599,8 @@ int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, voi
  *   workspace, ws_bytes  DEVICE scratch of at least
  *                   fathom_paged_attention_workspace_bytes() bytes for the
  *                   same H, G, D, rows, B, max_new, max_len, q_dtype, 256-byte
- *                   aligned (may be NULL when that is 0).  Used until the
- *                   call's work is done: calls that may overlap on the GPU
+ *                   aligned (may be NULL when that is 0, as it is for sizes
+ *                   that the call refuses).  Used until the call's work is done: calls that may overlap on the GPU
  *                   need one each.
  * Arithmetic: products of bf16 values summed in fp32, the softmax in fp32.
  * fp32 queries are taken as the sum of three bf16 parts (all 24 bits), and so

@@ -2,6 +2,8 @@
 // include/fathom.h): argument checks on the host, then the launches.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "args.cuh"
 #include "kv.cuh"
 
@@ -17,6 +19,10 @@ size_t paged_union_attention_workspace_bytes(int64_t H, int G, int D, int64_t M)
 int launch_paged_attention(const KvAttend& a, int format, int q_dtype, void* ws, cudaStream_t stream);
 
 namespace {
+
+constexpr int64_t kMaxTokens = 1LL << 30;                 // of a sequence: token + stretch stays an int
+constexpr int64_t kMaxQueryRows = (1LL << 31) - 1;        // of a sequence: rows times heads of a group
+constexpr int64_t kMaxRows = (1LL << 31) - 1, kMaxSequences = 65535;
 
 #define FATHOM_TRY(expr)                 \
     do {                                 \
@@ -42,7 +48,7 @@ int check_sizes(const fathom_kv_cache* c)
 
 int check_rows(const fathom_kv_rows* w)
 {
-    if (!w || w->B < 0 || w->B > 65535 || w->rows < 0 || w->rows >= (1LL << 31)) return FATHOM_ERR_INVALID_ARG;
+    if (!w || w->B < 0 || w->B > kMaxSequences || w->rows < 0 || w->rows > kMaxRows) return FATHOM_ERR_INVALID_ARG;
     if (w->table_pages < 0 || w->table_stride < 0) return FATHOM_ERR_INVALID_ARG;
     return FATHOM_OK;
 }
@@ -194,9 +200,9 @@ int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, voi
 size_t fathom_paged_attention_workspace_bytes(int H, int G, int D, int64_t rows, int B, int64_t max_new,
                                               int64_t max_len, int q_dtype)
 {
-    if (H <= 0 || H > 65535 || !dims_ok(D, G) || rows <= 0 || B <= 0 || max_new <= 0 || max_len <= 0 ||
-        !dtype_ok(q_dtype))
-        return 0;
+    if (H <= 0 || H > 65535 || !dims_ok(D, G) || rows <= 0 || rows > kMaxRows || B <= 0 || B > kMaxSequences || max_new <= 0 ||
+        max_len <= 0 || max_len > kMaxTokens || std::min(max_new, rows) * G > kMaxQueryRows || !dtype_ok(q_dtype))
+        return 0;   // sizes that the call refuses too: the cut counts tokens and query rows in ints
     return paged_attention_workspace_bytes(H, G, D, rows, B, max_new, max_len, q_dtype);
 }
 
@@ -210,10 +216,10 @@ int fathom_paged_attention(const fathom_kv_cache* cache, const fathom_kv_rows* r
     FATHOM_TRY(check_rows(rows));
     if (!dtype_ok(q_dtype) || q_stride_tok < 0 || q_stride_h < 0 || !scale_ok(scale)) return FATHOM_ERR_INVALID_ARG;
     if (max_new < 0 || max_len < 0) return FATHOM_ERR_INVALID_ARG;
-    if (G < 1 || G > kMaxG || max_len > (1LL << 30)) return FATHOM_ERR_UNSUPPORTED;   // token + stretch stays an int
+    if (G < 1 || G > kMaxG || max_len > kMaxTokens) return FATHOM_ERR_UNSUPPORTED;
     if (cache->H == 0 || rows->B == 0 || rows->rows == 0 || max_new == 0) return FATHOM_OK;
     if (max_new > rows->rows) max_new = rows->rows;
-    if (max_new * G >= (1LL << 31)) return FATHOM_ERR_UNSUPPORTED;
+    if (max_new * G > kMaxQueryRows) return FATHOM_ERR_UNSUPPORTED;
     const size_t need = fathom_paged_attention_workspace_bytes(cache->H, G, cache->D, rows->rows, rows->B, max_new,
                                                                max_len, q_dtype);
     if (ws_bytes < need) return FATHOM_ERR_WORKSPACE;

@@ -179,3 +179,16 @@ def test_workspace_that_is_not_what_it_says():
     wide = torch.zeros(1, dtype=torch.uint8).expand(1 << 20)   # one byte that calls itself a mebibyte
     with pytest.raises(ValueError, match="contiguous"):
         fathom._workspace(wide, 1 << 20, wide, None)
+
+
+def test_workspace_of_sizes_that_are_refused(lib):
+    """The query knows the bounds of the call: nothing to give for more tokens, query rows, rows or sequences than it takes."""
+    ws = lib.fathom_paged_attention_workspace_bytes
+    for max_len in ((1 << 30) + 1, 1 << 31, (1 << 32) - 1, 1 << 32, 1 << 33, 1 << 62):
+        for dtype in (0, 1):
+            for rows_, B, new in ((2, 2, 1), (300, 300, 1), (300, 1, 300), (90000, 300, 300), (5000, 1, 5000)):
+                assert ws(8, 4, 128, rows_, B, new, max_len, dtype) == 0
+    assert ws(8, 8, 128, (1 << 28) + 1, 1, 1 << 28, 1 << 20, 1) == 0          # rows of queries that no int counts
+    assert ws(1, 1, 128, 1 << 31, 1, 1, 1 << 20, 1) == 0 and ws(1, 1, 128, 1 << 62, 1, 1, 1 << 20, 1) == 0
+    assert ws(1, 1, 128, 10, 1 << 16, 1, 1 << 20, 1) == 0
+    assert ws(1, 1, 128, 1, 1, 1, 1 << 30, 1) > 0
