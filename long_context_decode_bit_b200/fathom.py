@@ -138,6 +138,23 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _scratch(stream, make, *args, **kw):
+    """A tensor made (``make(*args, **kw)``) for a call on ``stream``, in that stream's memory: a block of the current
+    one's may be free because only the order of that stream's work protects it."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _output(stream, make, *args, **kw):
+    """The same, of a tensor that is handed to the caller, whose own stream uses it once ``stream`` is done."""
+    t = _scratch(stream, make, *args, **kw)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def nb_stride(n: int) -> int:
     return int(lib().fathom_nb_stride(int(n)))
 
@@ -160,9 +177,9 @@ def pack(keys: torch.Tensor, nb_stride_words: int | None = None, planes=None, sc
     nbs = nb_stride(n) if nb_stride_words is None else int(nb_stride_words)
     dev = keys.device
     if planes is None:
-        planes = torch.zeros((H, D, 4, nbs), dtype=torch.int64, device=dev)
+        planes = _output(stream, torch.zeros, (H, D, 4, nbs), dtype=torch.int64, device=dev)
     if scales is None:
-        scales = torch.zeros((H, D, nbs), dtype=torch.int16, device=dev)
+        scales = _output(stream, torch.zeros, (H, D, nbs), dtype=torch.int16, device=dev)
     _check(lib().fathom_pack(_p(keys), dt, H, n, D, keys.stride(0), keys.stride(1), _p(planes), _p(scales),
                              nbs, _stream(stream)), "fathom_pack")
     return planes, scales
@@ -182,9 +199,9 @@ def pack_rotated(keys: torch.Tensor, U: torch.Tensor, nb_stride_words: int | Non
     nbs = nb_stride(n) if nb_stride_words is None else int(nb_stride_words)
     dev = keys.device
     if planes is None:
-        planes = torch.zeros((H, D, 4, nbs), dtype=torch.int64, device=dev)
+        planes = _output(stream, torch.zeros, (H, D, 4, nbs), dtype=torch.int64, device=dev)
     if scales is None:
-        scales = torch.zeros((H, D, nbs), dtype=torch.int16, device=dev)
+        scales = _output(stream, torch.zeros, (H, D, nbs), dtype=torch.int16, device=dev)
     _check(lib().fathom_pack_rotated(_p(keys), dt, H, n, D, keys.stride(0), keys.stride(1), _p(U), _p(planes),
                                      _p(scales), nbs, _stream(stream)), "fathom_pack_rotated")
     return planes, scales
@@ -215,8 +232,10 @@ def plan(sigma2: torch.Tensor, q: torch.Tensor, budget, out=None, stream=None):
     H, G, D = q.shape
     dev = q.device
     if out is None:
-        out = (torch.empty((H, D), dtype=torch.uint8, device=dev), torch.empty((H, D), dtype=torch.int16, device=dev),
-               torch.empty(H, dtype=torch.int32, device=dev), torch.empty(H, dtype=torch.float32, device=dev))
+        out = (_output(stream, torch.empty, (H, D), dtype=torch.uint8, device=dev),
+               _output(stream, torch.empty, (H, D), dtype=torch.int16, device=dev),
+               _output(stream, torch.empty, H, dtype=torch.int32, device=dev),
+               _output(stream, torch.empty, H, dtype=torch.float32, device=dev))
     depth, active, n_active, theta = out
     if isinstance(budget, torch.Tensor):
         bptr, flat = _p(budget), 0
@@ -233,8 +252,9 @@ def layer_budgets(sigma2: torch.Tensor, q: torch.Tensor, layers: int, total_bits
     H, G, D = q.shape
     dev = q.device
     if out is None:
-        out = torch.empty(H, dtype=torch.int32, device=dev)
-    ws = torch.empty(max(int(lib().fathom_layer_budgets_workspace_bytes(H, D)), 1), dtype=torch.uint8, device=dev)
+        out = _output(stream, torch.empty, H, dtype=torch.int32, device=dev)
+    need = int(lib().fathom_layer_budgets_workspace_bytes(H, D))
+    ws = _scratch(stream, torch.empty, max(need, 1), dtype=torch.uint8, device=dev)
     _check(lib().fathom_layer_budgets(_p(sigma2), _p(q), H, G, D, int(layers), int(total_bits), _p(out), _p(ws),
                                       ws.numel(), _stream(stream)), "fathom_layer_budgets")
     return out
@@ -246,8 +266,9 @@ def plan_fixed(q: torch.Tensor, r: int, out=None, stream=None, bits: int = 4):
     H, G, D = q.shape
     dev = q.device
     if out is None:
-        out = (torch.empty((H, D), dtype=torch.uint8, device=dev), torch.empty((H, D), dtype=torch.int16, device=dev),
-               torch.empty(H, dtype=torch.int32, device=dev))
+        out = (_output(stream, torch.empty, (H, D), dtype=torch.uint8, device=dev),
+               _output(stream, torch.empty, (H, D), dtype=torch.int16, device=dev),
+               _output(stream, torch.empty, H, dtype=torch.int32, device=dev))
     depth, active, n_active = out
     _check(lib().fathom_plan_fixed(_p(q), H, G, D, int(r), int(bits), _p(depth), _p(active), _p(n_active),
                                    _stream(stream)),
@@ -271,13 +292,13 @@ def scan(planes, scales, n: int, active, n_active, q, mode: int = SCAN_DENSE, k:
         fn, name = lib().fathom_scan, "fathom_scan"
     if mode == SCAN_DENSE:
         if scores is None:
-            scores = torch.empty((H, G, n), dtype=torch.float32, device=q.device)
+            scores = _output(stream, torch.empty, (H, G, n), dtype=torch.float32, device=q.device)
         _check(fn(_p(planes), _p(scales), H, D, n, nbs, _p(active), _p(n_active), _p(q), G,
                   SCAN_DENSE, _p(scores), None, 0, int(k), _stream(stream)), name)
         return scores
     nbytes = scan_cand_bytes(H, G, n, k)
     if cand is None:
-        cand = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        cand = _output(stream, torch.empty, nbytes, dtype=torch.uint8, device=q.device)
     _check(fn(_p(planes), _p(scales), H, D, n, nbs, _p(active), _p(n_active), _p(q), G,
               int(mode), None, _p(cand), cand.numel() * cand.element_size(), int(k), _stream(stream)), name)
     return cand
@@ -287,7 +308,7 @@ def nibbles_from_planes(planes, n: int, out=None, stream=None):
     """The nibble store [H][D][4][nb_stride] of the codes the planes hold."""
     H, D, _, nbs = planes.shape
     if out is None:
-        out = torch.empty_like(planes)
+        out = _output(stream, torch.empty_like, planes)
     _check(lib().fathom_nibbles_from_planes(_p(planes), H, D, n, nbs, _p(out), _stream(stream)),
            "fathom_nibbles_from_planes")
     return out
@@ -298,7 +319,7 @@ def nibbles_tm_from_planes(planes, n: int, out=None, stream=None):
     the planes hold (two channels per byte, channel 2c in the low nibble)."""
     H, D, _, nbs = planes.shape
     if out is None:
-        out = torch.zeros((H, 64 * nbs, D // 2), dtype=torch.uint8, device=planes.device)
+        out = _output(stream, torch.zeros, (H, 64 * nbs, D // 2), dtype=torch.uint8, device=planes.device)
     _check(lib().fathom_nibbles_tm_from_planes(_p(planes), H, D, n, nbs, _p(out), _stream(stream)),
            "fathom_nibbles_tm_from_planes")
     return out
@@ -309,13 +330,13 @@ def topk(H: int, G: int, n: int, k: int, scores=None, cand=None, out=None, works
     union int32 [H][G*k], union_count int32 [H])."""
     dev = (scores if scores is not None else cand).device
     if out is None:
-        out = (torch.empty((H, G, k), dtype=torch.int32, device=dev),
-               torch.empty((H, G * k), dtype=torch.int32, device=dev),
-               torch.empty(H, dtype=torch.int32, device=dev))
+        out = (_output(stream, torch.empty, (H, G, k), dtype=torch.int32, device=dev),
+               _output(stream, torch.empty, (H, G * k), dtype=torch.int32, device=dev),
+               _output(stream, torch.empty, H, dtype=torch.int32, device=dev))
     idx, uni, cnt = out
     ws_need = topk_workspace_bytes(H, G, n, k)
     if workspace is None and ws_need:
-        workspace = torch.empty(ws_need, dtype=torch.uint8, device=dev)
+        workspace = _scratch(stream, torch.empty, ws_need, dtype=torch.uint8, device=dev)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().fathom_topk(_p(scores), _p(cand), H, G, n, int(k), _p(idx), _p(uni), _p(cnt), _p(workspace),
                              ws_bytes, _stream(stream)), "fathom_topk")
@@ -328,7 +349,7 @@ def dequant_rows(planes, scales, n: int, rows, row_count=None, bits: int = 4, ou
     H, D = planes.shape[0], planes.shape[1]
     M = rows.shape[1]
     if out is None:
-        out = torch.empty((H, M, D), dtype=torch.float32, device=rows.device)
+        out = _output(stream, torch.empty, (H, M, D), dtype=torch.float32, device=rows.device)
     _check(lib().fathom_dequant_rows(_p(planes), _p(scales), H, D, n, planes.shape[-1], _p(rows), M,
                                      _p(row_count), int(bits), _p(out), _stream(stream)), "fathom_dequant_rows")
     return out
@@ -342,9 +363,9 @@ def scan_topk_noalloc(planes, scales, n: int, active, n_active, q, k: int, out=N
     H, G, D = q.shape
     if out is None:
         dev = q.device
-        out = (torch.empty((H, G, k), dtype=torch.int32, device=dev),
-               torch.empty((H, G * k), dtype=torch.int32, device=dev),
-               torch.empty(H, dtype=torch.int32, device=dev))
+        out = (_output(stream, torch.empty, (H, G, k), dtype=torch.int32, device=dev),
+               _output(stream, torch.empty, (H, G * k), dtype=torch.int32, device=dev),
+               _output(stream, torch.empty, H, dtype=torch.int32, device=dev))
     idx, uni, cnt = out
     _check(lib().fathom_scan_topk_noalloc(_p(planes), _p(scales), H, D, n, planes.shape[-1], _p(active),
                                           _p(n_active), _p(q), G, int(k), _p(idx), _p(uni), _p(cnt),
@@ -372,12 +393,12 @@ def calibrate(keys: torch.Tensor, n: int | None = None, with_mean: bool = True, 
     if keys.stride(2) != 1:
         raise ValueError("keys must be contiguous along D")
     dev = keys.device
-    sigma2 = torch.empty((H, D), dtype=torch.float32, device=dev)
-    mean = torch.empty((H, D), dtype=torch.float32, device=dev) if with_mean else None
-    cov = torch.empty((H, D, D), dtype=torch.float32, device=dev) if with_cov else None
+    sigma2 = _output(stream, torch.empty, (H, D), dtype=torch.float32, device=dev)
+    mean = _output(stream, torch.empty, (H, D), dtype=torch.float32, device=dev) if with_mean else None
+    cov = _output(stream, torch.empty, (H, D, D), dtype=torch.float32, device=dev) if with_cov else None
     need = calibrate_workspace_bytes(H, D, with_cov)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = _scratch(stream, torch.empty, max(need, 1), dtype=torch.uint8, device=dev)
     _check(lib().fathom_calibrate(_p(keys), dt, H, n, D, keys.stride(0), keys.stride(1), _p(mean), _p(sigma2),
                                   _p(cov), _p(workspace), workspace.numel(), _stream(stream)), "fathom_calibrate")
     return mean, sigma2, cov
@@ -400,10 +421,10 @@ def union_attention(k_cache: torch.Tensor, v_cache: torch.Tensor, q: torch.Tenso
     if k_cache.stride(2) != 1:
         raise ValueError("the cache must be contiguous along D")
     if out is None:
-        out = torch.empty((H, G, D), dtype=torch.float32, device=q.device)
+        out = _output(stream, torch.empty, (H, G, D), dtype=torch.float32, device=q.device)
     need = int(lib().fathom_union_attention_workspace_bytes(H, G, D, M))
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(stream, torch.empty, max(need, 1), dtype=torch.uint8, device=q.device)
     sc = 1.0 / math.sqrt(D) if scale is None else float(scale)
     _check(lib().fathom_union_attention(_p(k_cache), _p(v_cache), dt, H, n, D, k_cache.stride(0), k_cache.stride(1),
                                         _p(q), G, _p(union_idx), _p(union_count), M, sc, _p(out), _p(workspace),
@@ -565,25 +586,22 @@ _paged_workspace = functools.lru_cache(1024)(lambda *sizes: lib().fathom_paged_a
 _union_workspace = functools.lru_cache(1024)(lambda *sizes: lib().fathom_paged_union_attention_workspace_bytes(*sizes))
 
 
-def _on(t, stream):
-    """A tensor made for a call: the call may be on another stream than the
-    current one, which the memory belongs to."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def _new(cache, shape, dtype, stream):
     """A contiguous [a][b][c] tensor (``empty_strided`` takes the host two
     thirds of the time that ``empty`` takes with a shape)."""
     _, b, c = shape
-    return _on(torch.empty_strided(shape, (b * c, c, 1), dtype=dtype, device=cache.k.device), stream)
+    if stream is None:
+        return torch.empty_strided(shape, (b * c, c, 1), dtype=dtype, device=cache.k.device)
+    return _output(stream, torch.empty_strided, shape, (b * c, c, 1), dtype=dtype, device=cache.k.device)
 
 
 def _workspace(workspace, need: int, like, stream):
     if workspace is None:
-        workspace = _on(like.new_empty(need, dtype=torch.uint8), stream) if need else None
-        return workspace, None if workspace is None else workspace.data_ptr(), need
+        if not need:
+            return None, None, 0
+        workspace = like.new_empty(need, dtype=torch.uint8) if stream is None else \
+            _scratch(stream, like.new_empty, need, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), need
     if not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
