@@ -564,7 +564,8 @@ typedef struct fathom_kv_rows {
  *                   group h, channel j at [r*stride_tok + h*stride_h + j].
  * The pages written must not be shared by two sequences of the call: of
  * two rows for one place each block keeps either's codes and scale, not
- * always of the same one.
+ * always of the same one.  rows*H*(D/16) at most (2^31 - 1)*256
+ * (ERR_UNSUPPORTED beyond).
  */
 int fathom_kv_write(const fathom_kv_cache* cache, const fathom_kv_rows* rows, const void* k, const void* v,
                     int dtype, int64_t stride_tok, int64_t stride_h, fathom_stream_t stream);

@@ -10,6 +10,7 @@ namespace fathom {
 
 constexpr int kKvBlock = 32;     // channels that share a power of two
 constexpr int kKvLowest = -100;  // smallest exponent kept
+constexpr int kKvThreads = 256;  // of a CTA that writes or reads rows
 
 struct KvCache {
     const unsigned char* k;
@@ -44,6 +45,9 @@ struct KvAttend {
     float scale;
     int G, causal;
 };
+
+// CTAs of a write: a thread takes 16 channels of a row.
+inline int64_t kv_write_ctas(int64_t rows, int H, int D) { return ceil_div(rows * H * (D / 16), kKvThreads); }
 
 // Bytes of a cached element.
 template <int FMT>

@@ -161,7 +161,7 @@ int fathom_kv_write(const fathom_kv_cache* cache, const fathom_kv_rows* rows, co
     FATHOM_TRY(check_rows(rows));
     if (!dtype_ok(dtype) || stride_tok < 0 || stride_h < 0) return FATHOM_ERR_INVALID_ARG;
     if (cache->H == 0 || rows->B == 0 || rows->rows == 0) return FATHOM_OK;
-    if (ceil_div(rows->rows * cache->H * (cache->D / 8), 256) > 0x7FFFFFFF) return FATHOM_ERR_UNSUPPORTED;
+    if (kv_write_ctas(rows->rows, cache->H, cache->D) > 0x7FFFFFFF) return FATHOM_ERR_UNSUPPORTED;
     if (!aligned(k, dtype_bytes(dtype)) || !aligned(v, dtype_bytes(dtype))) return FATHOM_ERR_UNSUPPORTED;
     KvCache c;
     KvRows w;

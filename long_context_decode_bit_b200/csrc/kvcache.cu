@@ -21,8 +21,6 @@ namespace fathom {
 
 namespace {
 
-constexpr int kKvThreads = 256;
-
 __device__ __forceinline__ void ld_global32(const void* p, uint4* u)
 {
     asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
@@ -300,7 +298,7 @@ template <int FMT, int DT, int VEC>
 int launch_kv_write_v(const KvCache& c, const KvRows& w, const void* k, const void* v, int64_t stride_tok, int64_t stride_h,
                       cudaStream_t stream)
 {
-    const unsigned grid = static_cast<unsigned>(ceil_div(static_cast<int64_t>(w.rows) * c.H * (c.D / 16), kKvThreads));
+    const unsigned grid = static_cast<unsigned>(kv_write_ctas(w.rows, c.H, c.D));
     kv_write_kernel<FMT, DT, VEC><<<grid, kKvThreads, 0, stream>>>(c, w, k, v, stride_tok, stride_h);
     return launch_status();
 }

@@ -192,3 +192,16 @@ def test_workspace_of_sizes_that_are_refused(lib):
     assert ws(1, 1, 128, 1 << 31, 1, 1, 1 << 20, 1) == 0 and ws(1, 1, 128, 1 << 62, 1, 1, 1 << 20, 1) == 0
     assert ws(1, 1, 128, 10, 1 << 16, 1, 1 << 20, 1) == 0
     assert ws(1, 1, 128, 1, 1, 1, 1 << 30, 1) > 0
+
+
+def test_largest_write(lib):
+    """A write is refused for its size where its CTAs pass what a launch takes, and only there (of two faults the size's is
+    reported first; these pointers are the other)."""
+    wide = dict(H=65535, D=256, token_stride=256, head_stride=64 * 256, page_stride=65535 * 64 * 256, scale_token_stride=8,
+                scale_head_stride=64 * 8, scale_page_stride=65535 * 64 * 8)
+
+    def write(n):   # n * 65535 * 16 threads, 256 to a CTA
+        return lib.fathom_kv_write(cache(**wide), rows(rows=n), FAKE, FAKE, 1, 65535 * 256, 256, None)
+    most = ((1 << 31) - 1) * 16 // 65535
+    assert write(300000) == write(most) == fathom.ERR_INVALID_ARG
+    assert write(most + 1) == fathom.ERR_UNSUPPORTED
