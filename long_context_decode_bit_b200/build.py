@@ -3,13 +3,15 @@
 ``python -m long_context_decode_bit_b200.build [--force] [--ptxas-v] [--test-hooks]``
 
 ``--test-hooks`` builds ``libfathom_testhooks.so`` instead: the same sources
-with a short ring-wait poll limit, the device-side bounds checks of
-``FATHOM_DEBUG_BOUNDS`` (a failed check sets the fault word's bounds bit and
-skips the access; ``fathom_device_status`` then returns FATHOM_ERR_BOUNDS),
-and two switches for tests: ``FATHOM_TEST_WITHHOLD_ARRIVAL=1`` makes the
-scan withhold one ring arrival (a bounded wait runs out), and
-``FATHOM_TEST_SHRINK_CAP=1`` makes the checks allow only half of the
-candidate entries (a check fails).  The product never loads it.
+with a short limit on the polls of a bounded wait, the device-side bounds
+checks of ``FATHOM_DEBUG_BOUNDS`` (a failed check sets the fault word's bounds
+bit and skips the access; ``fathom_device_status`` then returns
+FATHOM_ERR_BOUNDS), and switches for tests: ``FATHOM_TEST_WITHHOLD_ARRIVAL=1``
+makes the scan withhold one ring arrival and ``FATHOM_TEST_WITHHOLD_TILE=i``
+the paged attention's chunk kernel one arrival for its i-th tile of K or V (a
+bounded wait runs out), and ``FATHOM_TEST_SHRINK_CAP=1`` makes the checks
+allow only half of the candidate entries (a check fails).  The product never
+loads it.
 """
 from __future__ import annotations
 

@@ -1,5 +1,7 @@
 // fathom_paged_attention and fathom_paged_union_attention: how a call is cut
 // up, and the joining of its stretches.
+#include <stdlib.h>
+
 #include <algorithm>
 
 #include "kvchunk.cuh"
@@ -202,6 +204,12 @@ int launch_paged_attention(const KvAttend& a, int format, int q_dtype, void* ws,
     g.a = a;
     g.s = a.uni ? union_split(a.c.H, a.M) : rows_split(a.c.H, a.G, a.c.D, a.w.rows, a.w.B, a.max_new, a.max_len, q_dtype);
     g.heads = static_cast<int64_t>(a.w.rows) * a.c.H * a.G;
+#ifdef FATHOM_TEST_HOOKS
+    {
+        const char* e = getenv("FATHOM_TEST_WITHHOLD_TILE");
+        g.withhold = e != nullptr ? atoi(e) : -1;
+    }
+#endif
     unsigned char* base = static_cast<unsigned char*>(ws);
     if (g.s.splits > 1) {
         g.po = reinterpret_cast<float*>(base);

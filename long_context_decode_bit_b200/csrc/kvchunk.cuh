@@ -223,14 +223,25 @@ __device__ __forceinline__ int64_t chunk_off(const KvCache& c, int page, int at,
 // The whole tiles of K and V from `begin` on, in the order K0 V0 K1 V1 ..., into the ring.
 // D is the width of the operands, c.D (less where not FULL) that of the rows.
 template <int D, int FMT, bool FULL>
-__device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* table, int table_pages, int h, int begin, int end,
-                                           uint32_t ring, uint32_t full, uint32_t empty)
+__device__ __forceinline__ bool chunk_load(const KvRowsArgs& g, const int32_t* table, int h, int begin, int end, uint32_t ring,
+                                           uint32_t full, uint32_t empty)
 {
+    const KvCache& c = g.a.c;
+    const int table_pages = g.a.w.table_pages;
     using S = ChunkShape<D, FMT>;
     constexpr int KEYS = S::KEYS;
     constexpr uint32_t ALL = (1u << (KEYS / 16)) - 1;
     const int t = threadIdx.x & 127, lane = threadIdx.x & 31;
     const int tiles = (end - begin + KEYS - 1) / KEYS;
+    // This thread's part of tile k is in its place.
+    auto filled = [&](int k) {
+#ifdef FATHOM_TEST_HOOKS
+        // Test build only: one thread of the first CTA of group 0 withholds its arrival for one tile, so that the waits on
+        // it run out, and those on what would follow.
+        if (k == g.withhold && t == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) return;
+#endif
+        mbar_arrive(full + 8 * (k % S::STAGES));
+    };
     bool ok = true;
     int page = chunk_page(c, table, table_pages, begin, end, lane);
     if constexpr (FMT == FATHOM_KV_BF16) {
@@ -268,18 +279,18 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
                 if (i == 1) {   // the first scores need not wait for what follows
                     asm volatile("cp.async.wait_group 1;\n" ::: "memory");
                     fence_async_smem();
-                    mbar_arrive(full);
+                    filled(0);
                 } else if (i > AHEAD) {
                     asm volatile("cp.async.wait_group %0;\n" ::"n"(AHEAD) : "memory");
                     fence_async_smem();
-                    mbar_arrive(full + 8 * ((i - AHEAD) % S::STAGES));
+                    filled(i - AHEAD);
                 }
             }
         }
         cp_async_wait_all();
         fence_async_smem();
         if (ok)
-            for (int k = max(1, i - AHEAD); k < i; ++k) mbar_arrive(full + 8 * (k % S::STAGES));
+            for (int k = max(1, i - AHEAD); k < i; ++k) filled(k);
     } else {
         // A thread copies 16-code pieces lq, lq + 4, ... of the rows lr, lr + 32, ... to a place of its own some tiles ahead, and decodes those same pieces from there.
         constexpr int KP = D / 64, RP = KEYS / 32, SW = 4 / RP, AHEAD = S::RAWS - 1;   // SW words of exponents to a row
@@ -362,7 +373,7 @@ __device__ __forceinline__ bool chunk_load(const KvCache& c, const int32_t* tabl
                                                        decode2<FMT, 0, 1>(w[3], w[3], f, masks), decode2<FMT, 2, 3>(w[3], w[3], f, masks)));
                 }
             fence_async_smem();
-            mbar_arrive(full + 8 * st);
+            filled(i);
         }
         cp_async_wait_all();
     }
@@ -520,7 +531,7 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
         __syncwarp();
     } else if (warp >= 8) {
         regs_down<kRegsLoad>();
-        if (!chunk_load<D, FMT, FULL>(a.c, table, a.w.table_pages, h, begin, end, ring, full, empty)) atomicOr(fault, kFaultTimeout);
+        if (!chunk_load<D, FMT, FULL>(g, table, h, begin, end, ring, full, empty)) atomicOr(fault, kFaultTimeout);
     } else {
         regs_up<kRegsSoftmax>();
         {   // Q, by all these warps

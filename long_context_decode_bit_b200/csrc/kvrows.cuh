@@ -51,6 +51,9 @@ struct KvRowsArgs {
     float* pm;   // [splits][rows*H*G] maxima (in powers of two)
     float* pl;   // [splits][rows*H*G] weight sums
     int64_t heads;   // rows*H*G
+#ifdef FATHOM_TEST_HOOKS
+    int32_t withhold;   // test build: tile of K or V (in the order they are brought) whose arrival is withheld, or -1
+#endif
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
