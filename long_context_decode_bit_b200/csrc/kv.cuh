@@ -179,4 +179,12 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return r;
 }
 
+// The same, rounded towards zero.
+__device__ __forceinline__ uint32_t bf16x2_cut(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 }  // namespace fathom

@@ -93,13 +93,14 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t f, const CodeMasks& 
     }
 }
 
-// x as bf16 parts that sum to it (to 8 bits each).
+// x as bf16 parts that sum to it (to 8 bits each).  Several parts are cut off rather than rounded: 8 bits of the 24 each,
+// so that nothing is lost, and the first of a value next to the largest is not an infinity.
 template <int N>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&part)[N])
 {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        part[i] = bf16x2(x, y);
+        part[i] = N > 1 ? bf16x2_cut(x, y) : bf16x2(x, y);
         x -= __uint_as_float(part[i] << 16);
         y -= __uint_as_float(part[i] & 0xffff0000u);
     }
