@@ -610,8 +610,10 @@ int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, voi
  * unrounded ones.  The result does not depend on timing.
  * Cached values of tokens below length should be finite where rows that do not
  * see them are to stay finite; what lies beyond length in a page is never
- * used.  A row that sees a NaN is NaN.  E4M3 codes that are NaN (0x7f, 0xff;
- * never written by fathom_kv_write) must not be in the cache.
+ * used.  A row that sees a NaN is NaN; a value that is infinite makes its
+ * channel infinite or NaN (fp32 queries: a part of a weight may be 0).  E4M3
+ * codes that are NaN (0x7f, 0xff) and exponent bytes outside a format's range
+ * but 255 are never written by fathom_kv_write and must not be in the cache.
  * 1 <= G <= 8; max_len <= 2^30; min(max_new, rows)*G < 2^31 (ERR_UNSUPPORTED
  * beyond).  bf16 queries of more than 32 rows*G run on a kernel with bounded
  * waits between its warps: should one run out, which takes a fault, the call's

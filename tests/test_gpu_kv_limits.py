@@ -34,3 +34,68 @@ def test_largest_fp32_queries(fathom_gpu, fmt, D, new):
     got = fathom_gpu.paged_union_attention(cache, q[-1:].contiguous(), table, 300, idx, torch.tensor([300], dtype=torch.int32, device=DEV),
                                            scale=scale)
     check_attention(got, tuple(x[-1:] for x in ref), 300, D, torch.float32)
+
+
+def bf16_of(x):
+    """Nearest bf16 value of fp32 values in 64 bits, ties to even (beyond the largest: infinity), NaN as NaN."""
+    with np.errstate(all="ignore"):
+        a = np.abs(x.astype(np.float64))
+        step = np.exp2(np.maximum(np.floor(np.log2(np.where((a > 0) & np.isfinite(a), a, 1.0))), -126) - 7)
+        y = np.where(np.isfinite(a), np.rint(a / step) * step, a)
+    return np.copysign(np.where(y >= 2.0 ** 128, np.inf, y), x)
+
+
+@pytest.mark.parametrize("shift", [0, 1])   # rows on 16 bytes, and not
+def test_bf16_pages_keep_infinities_and_nan(fathom_gpu, shift):
+    """What a bf16 cache holds of infinities, NaN, values around the largest and the least, and ties; the channels beside
+    them are as they were."""
+    f = np.float32
+    ends = np.array([np.inf, -np.inf, np.nan, 3.3895314e38, 3.39615e38, np.nextafter(f(3.3961775e38), f(0)), 3.3961775e38, 3.4028235e38,
+                     -3.4028235e38, 1e-45, -1e-45, 9.2e-41, 4.6e-41, 1.1754944e-38, 1.1754942e-38, 0.0, -0.0, 1.00390625,
+                     1.01171875, -1.00390625], f)
+    x = np.random.default_rng(3).standard_normal((len(ends) + 3, 2, 64)).astype(f)
+    for i, e in enumerate(ends):
+        x[i, 0, (7 * i) % 64] = e
+        x[i, 1, (11 * i + 5) % 64] = e
+    n = len(x)
+    pages, table, cu, length = make_batch([(n, n)], 16)
+    args = table.cpu().numpy(), cu.cpu().numpy(), length.cpu().numpy()
+    for dtype in (torch.float32, torch.bfloat16):
+        cache = make_cache(fathom_gpu, "bf16", pages, 2, 64, 16)
+        wide = torch.zeros(n, 2, 64 + 8, device=DEV, dtype=dtype)
+        rows = wide[..., shift:shift + 64]
+        rows.copy_(torch.tensor(x))
+        fathom_gpu.kv_write(cache, rows, rows, table, cu, length)
+        want = bf16_of(x).transpose(1, 0, 2)
+        for got in okv.read(host(cache), "bf16", *args, n):
+            assert np.array_equal(got, want, equal_nan=True)
+        for out in (torch.float32, torch.bfloat16):
+            for got in fathom_gpu.kv_read(cache, table, cu, length, n, dtype=out):
+                assert np.array_equal(got.float().cpu().numpy().astype(np.float64), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("new", [1, 60])
+def test_infinities_in_bf16_pages(fathom_gpu, new):
+    """A value that is infinite makes its channel of the rows that see it infinite (or NaN, of fp32 queries), and NaN where
+    there is one of the other sign; a key that is infinite makes them NaN (its score and the largest one are).  Rows of other sequences stay."""
+    lens = [(new, new + 20), (new, new + 20), (new, 90)]
+    pages, table, cu, length = make_batch(lens, 16)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    n = sum(t for _, t in lens)
+    k, v = (torch.randn((n, 1, 64), generator=g, device=DEV) for _ in range(2))
+    v[3, 0, 5], v[4, 0, 6], v[5, 0, 6] = np.inf, np.inf, -np.inf        # sequence 0
+    k[new + 20 + 2] = np.inf                                             # sequence 1
+    cache = make_cache(fathom_gpu, "bf16", pages, 1, 64, 16)
+    everything = torch.tensor([0, new + 20, 2 * new + 40, n], dtype=torch.int32, device=DEV)
+    fathom_gpu.kv_write(cache, k, v, table, everything, length)
+    for dt in (torch.float32, torch.bfloat16):
+        q = torch.randn((3 * new, 4, 64), generator=g, device=DEV).abs().to(dt)   # that key's score is infinite
+        out = fathom_gpu.paged_attention(cache, q, table, cu, length, new, 90).float()
+        first = out[:new]
+        # Of fp32 queries a weight is three parts, and where it has no more than 16 bits the last is 0: 0 * inf is NaN.
+        assert ((first[..., 5] == np.inf) | (first[..., 5].isnan() & (dt == torch.float32))).all()
+        assert first[..., 6].isnan().all()
+        rest = torch.ones(64, dtype=torch.bool, device=DEV)
+        rest[5:7] = False
+        assert first[..., rest].isfinite().all()
+        assert out[new:2 * new].isnan().all() and out[2 * new:].isfinite().all()
