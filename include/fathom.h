@@ -606,8 +606,8 @@ int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, voi
  * Arithmetic: products of bf16 values summed in fp32, the softmax in fp32.
  * fp32 queries are taken as the sum of three bf16 parts (all 24 bits), and so
  * are the weights exp(s - max) that enter the value product; with bf16 queries
- * they enter it in bf16 (half a step, 2^-9 of a weight) and their sum is of the
- * unrounded ones.  The result does not depend on timing.
+ * they enter it in bf16 (half a step, up to 2^-8 of a weight) and their sum is
+ * of the unrounded ones.  The result does not depend on timing.
  * Cached values of tokens below length should be finite where rows that do not
  * see them are to stay finite; what lies beyond length in a page is never
  * used.  A row that sees a NaN is NaN; a value that is infinite makes its

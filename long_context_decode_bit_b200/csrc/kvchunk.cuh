@@ -23,8 +23,9 @@
 // The running maximum m of a row is raised only when it grew by more than
 // 2^8 (P and l then stay below 2^8 times what the true maximum gives, far
 // inside bf16's and fp32's range), so O is rarely touched between products.
-// P enters the product in bf16 (relative 2^-9 to a weight); l sums the
-// unrounded weights in fp32.
+// P enters the product in bf16 (off by up to 2^-8 of a weight); l sums the
+// unrounded weights in fp32.  (A second part would be half as many products
+// again, on a kernel whose products are active two thirds of the time.)
 //
 // Every wait on a barrier has an iteration limit; a role whose wait runs out
 // sets the fault word and leaves its loop, and the CTA frees its tensor memory.
@@ -736,7 +737,7 @@ int launch_chunk_t(const KvRowsArgs& g, cudaStream_t stream)
     return launch_status();
 }
 
-// kvchunk.cu: chunks of bf16 queries over caches of up to 128 channels.
+// kvchunk.cu: chunks of bf16 queries over caches of 32 to 256 channels (widths between 64, 128 and 256 with zeros behind).
 int launch_chunk(const KvRowsArgs& g, int format, cudaStream_t stream);
 
 }  // namespace fathom
