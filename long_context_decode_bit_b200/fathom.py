@@ -458,7 +458,10 @@ class KVCache:
     include/fathom.h): k, v [pages][H][page_tokens][D] in bf16, int8 or
     float8_e4m3fn (any strides, channels contiguous; ``transpose(1, 2)`` of a
     [pages][page_tokens][H][D] tensor, or one layer of a larger one), and for
-    the 8-bit formats k_scale, v_scale uint8 [pages][H][page_tokens][D/32]."""
+    the 8-bit formats k_scale, v_scale uint8 [pages][H][page_tokens][D/32].
+    Their addresses are taken once, so none of its attributes can be replaced."""
+
+    _FIXED = frozenset(("k", "v", "k_scale", "v_scale", "H", "D", "page_tokens", "format", "_struct", "_ref", "_device"))
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale=None, v_scale=None):
         if k.dtype not in _KV_FORMATS:
@@ -485,8 +488,18 @@ class KVCache:
         self._struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), *scale_ptr, pages, k.stride(0), k.stride(1),
                                       k.stride(2), strides[0], strides[1], strides[2], self.H, self.D,
                                       self.page_tokens, self.format)
-        self._ref = ctypes.byref(self._struct)
         self._device = k.get_device()   # -1: not on a GPU
+        self._ref = ctypes.byref(self._struct)
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED and "_ref" in self.__dict__:
+            raise AttributeError(f"{name} is part of what calls use; make another KVCache")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        if name in self._FIXED:
+            raise AttributeError(f"{name} is part of what calls use; make another KVCache")
+        super().__delattr__(name)
 
     @classmethod
     def empty(cls, pages: int, H: int, D: int, page_tokens: int = 64, dtype=torch.int8, device="cuda"):

@@ -205,3 +205,19 @@ def test_largest_write(lib):
     most = ((1 << 31) - 1) * 16 // 65535
     assert write(300000) == write(most) == fathom.ERR_INVALID_ARG
     assert write(most + 1) == fathom.ERR_UNSUPPORTED
+
+
+def test_a_cache_keeps_its_tensors():
+    """The addresses that calls use are those of the tensors it was made over: another tensor in an attribute's place would
+    leave them pointing at freed memory."""
+    k, s = torch.zeros(4, 2, 16, 64, dtype=torch.int8), torch.zeros(4, 2, 16, 2, dtype=torch.uint8)
+    c = fathom.KVCache(k, k.clone(), s, s.clone())
+    for name in ("k", "v", "k_scale", "v_scale", "H", "D", "page_tokens", "format"):
+        old = getattr(c, name)
+        with pytest.raises(AttributeError, match="another KVCache"):
+            setattr(c, name, old.clone() if isinstance(old, torch.Tensor) else old)
+        assert getattr(c, name) is old
+        with pytest.raises(AttributeError):
+            delattr(c, name)
+    c.label = "a user's own"
+    assert c._struct.k == c.k.data_ptr() and c._struct.v_scale == c.v_scale.data_ptr()
