@@ -631,7 +631,7 @@ def paged_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, cu: to
     if dt is None:
         raise TypeError("q is float32 or bfloat16")
     shape, strides = q.shape, q.stride()
-    if len(shape) != 3 or shape[2] != cache.D or shape[1] % cache.H or strides[2] != 1:
+    if len(shape) != 3 or shape[2] != cache.D or not cache.H or shape[1] % cache.H or strides[2] != 1:
         raise ValueError("q must be [rows][H*G][D], contiguous along D")
     rows, G = shape[0], shape[1] // cache.H
     if out is None:

@@ -221,3 +221,12 @@ def test_a_cache_keeps_its_tensors():
             delattr(c, name)
     c.label = "a user's own"
     assert c._struct.k == c.k.data_ptr() and c._struct.v_scale == c.v_scale.data_ptr()
+
+
+def test_cache_of_no_groups():
+    k, s = torch.zeros(4, 0, 16, 64, dtype=torch.int8), torch.zeros(4, 0, 16, 2, dtype=torch.uint8)
+    c = fathom.KVCache(k, k.clone(), s, s.clone())
+    table, cu, length = torch.zeros(1, 4, dtype=torch.int32), torch.tensor([0, 3], dtype=torch.int32), torch.tensor([3], dtype=torch.int32)
+    for heads in (0, 4):
+        with pytest.raises(ValueError, match=r"q must be \[rows\]"):
+            fathom.paged_attention(c, torch.zeros(3, heads, 64), table, cu, length, 3, 3)
