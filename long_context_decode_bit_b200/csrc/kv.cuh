@@ -20,6 +20,10 @@ struct KvCache {
     int64_t page_stride, head_stride, token_stride;      // bytes
     int64_t spage_stride, shead_stride, stoken_stride;   // bytes
     int32_t pages, H, D, page_tokens, page_shift;
+#ifdef FATHOM_DEBUG_BOUNDS
+    int64_t bytes, scale_bytes;   // from the first to behind the last byte of K or V, and of their exponents
+    int32_t* fault;
+#endif
 };
 
 struct KvRows {
@@ -70,6 +74,35 @@ __device__ __forceinline__ int64_t kv_off(const KvCache& c, int page, int h, int
 __device__ __forceinline__ int64_t kv_scale_off(const KvCache& c, int page, int h, int token)
 {
     return page * c.spage_stride + h * c.shead_stride + token * c.stoken_stride;
+}
+
+// Debug build: `n` bytes `off` from the start of K or V, or of their exponents, are the cache's (bounds_ok).
+__device__ __forceinline__ bool kv_in(const KvCache& c, int64_t off, int n)
+{
+#ifdef FATHOM_DEBUG_BOUNDS
+    return bounds_ok(off >= 0 && off + n <= c.bytes, c.fault);
+#else
+    return true;
+#endif
+}
+
+__device__ __forceinline__ bool kv_scale_in(const KvCache& c, int64_t off, int n)
+{
+#ifdef FATHOM_DEBUG_BOUNDS
+    return bounds_ok(off >= 0 && off + n <= c.scale_bytes, c.fault);
+#else
+    return true;
+#endif
+}
+
+// The same of place `at` of the `n` that an output or a call's scratch has.
+__device__ __forceinline__ bool kv_place_in(const KvCache& c, int64_t at, int64_t n)
+{
+#ifdef FATHOM_DEBUG_BOUNDS
+    return bounds_ok(at >= 0 && at < n, c.fault);
+#else
+    return true;
+#endif
 }
 
 // Sequence of row r (cu[b] <= r < cu[b+1]), or -1: the last b whose cu[b] <= r.

@@ -1,6 +1,7 @@
 // extern "C" entry points of the paged KV cache (declared in
 // include/fathom.h): argument checks on the host, then the launches.
 #include <cuda.h>
+#include <stdlib.h>
 
 #include <algorithm>
 
@@ -130,6 +131,20 @@ int check_cache(const fathom_kv_cache* c, KvCache* out)
     out->page_tokens = c->page_tokens;
     out->page_shift = 0;
     while ((1 << out->page_shift) < c->page_tokens) ++out->page_shift;
+#ifdef FATHOM_DEBUG_BOUNDS
+    FATHOM_TRY(device_fault_word(&out->fault));
+    auto bytes = [&](int64_t page, int64_t head, int64_t token, int64_t row) {
+        return c->pages ? (c->pages - 1) * page + (c->H - 1) * head + (c->page_tokens - 1) * token + row : 0;
+    };
+    out->bytes = bytes(out->page_stride, out->head_stride, out->token_stride, c->D * esz);
+    out->scale_bytes = coded ? bytes(out->spage_stride, out->shead_stride, out->stoken_stride, c->D / kKvBlock) : 0;
+    // Test build only: let the checks allow half of the cache, so that a test sees a failed one reach the host.
+    const char* e = getenv("FATHOM_TEST_SHRINK_CAP");
+    if (e != nullptr && e[0] == '1') {
+        out->bytes /= 2;
+        out->scale_bytes /= 2;
+    }
+#endif
     return FATHOM_OK;
 }
 

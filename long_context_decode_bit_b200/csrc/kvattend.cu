@@ -137,6 +137,7 @@ kv_join_kernel(const KvRowsArgs g)
 #pragma unroll 4
     for (int s = warp; s < n; s += WARPS) {
         const int64_t at = s * g.heads + head;
+        if (!kv_place_in(a.c, at, g.s.splits * g.heads)) continue;
         const float f = exp2_fast(g.pm[at] - low);
         l += g.pl[at] * f;
 #pragma unroll

@@ -193,7 +193,7 @@ kv_write_kernel(const KvCache c, const KvRows w, const void* __restrict__ k, con
         float y[16];
         kv_values<DT>(x[s], y);
         if (FMT == FATHOM_KV_BF16) {
-            if (live) {
+            if (live && kv_in(c, to + 2 * j, 32)) {
                 uint4* o = reinterpret_cast<uint4*>(data + to + 2 * j);
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
@@ -203,10 +203,11 @@ kv_write_kernel(const KvCache c, const KvRows w, const void* __restrict__ k, con
         } else {
             uint32_t byte;
             const uint4 codes = kv_encode16<FMT>(y, kv_largest<DT>(x[s]), &byte);
-            if (live) {
+            if (live && kv_in(c, to + j, 16)) {
                 *reinterpret_cast<uint4*>(data + to + j) = codes;
                 unsigned char* sc = const_cast<unsigned char*>(s ? c.vs : c.ks);
-                if ((j & 31) == 0) sc[kv_scale_off(c, page, h, token) + (j >> 5)] = static_cast<unsigned char>(byte);
+                const int64_t at = kv_scale_off(c, page, h, token) + (j >> 5);
+                if ((j & 31) == 0 && kv_scale_in(c, at, 1)) sc[at] = static_cast<unsigned char>(byte);
             }
         }
     }
@@ -267,10 +268,16 @@ kv_read_kernel(const KvCache c, const KvRows w, void* out_k, void* out_v, int64_
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         if (page >= 0 && (s ? out_v : out_k)) {
-            const uint4* from = reinterpret_cast<const uint4*>((s ? c.v : c.k) + kv_off(c, page, h, token) + j * kv_elem_bytes<FMT>());
+            const int64_t at = kv_off(c, page, h, token) + j * kv_elem_bytes<FMT>();
+            const uint4* from = reinterpret_cast<const uint4*>((s ? c.v : c.k) + at);
+            if (kv_in(c, at, 16 * PIECES)) {
 #pragma unroll
-            for (int q = 0; q < PIECES; ++q) raw[s][q] = __ldg(from + q);
-            if (FMT != FATHOM_KV_BF16) byte[s] = __ldg((s ? c.vs : c.ks) + kv_scale_off(c, page, h, token) + (j >> 5));
+                for (int q = 0; q < PIECES; ++q) raw[s][q] = __ldg(from + q);
+            }
+            if (FMT != FATHOM_KV_BF16) {
+                const int64_t sat = kv_scale_off(c, page, h, token) + (j >> 5);
+                if (kv_scale_in(c, sat, 1)) byte[s] = __ldg((s ? c.vs : c.ks) + sat);
+            }
         }
     }
     const int64_t to = h * stride_h + row * stride_tok + j;

@@ -270,9 +270,9 @@ __device__ __forceinline__ bool chunk_load(const KvRowsArgs& g, const int32_t* t
                     // p*ROWS rows behind; where ROWS is 4, every other time 4 chunks on in the swizzle
                     const uint32_t to = ((to0 + st * S::TILE) ^ ((p * ROWS & 7) << 4)) + p * ROWS * 128;
                     if (whole) {
-                        cp_async16_to(to, from);
+                        if (kv_in(c, from - data, 16)) cp_async16_to(to, from);
                     } else {
-                        const bool live = there && o >= 0 && at + r0 + p * ROWS < end;
+                        const bool live = there && o >= 0 && at + r0 + p * ROWS < end && kv_in(c, from - data, 16);
                         cp_async16_to(to, live ? from : data, live ? 16 : 0);
                     }
                 }
@@ -324,12 +324,12 @@ __device__ __forceinline__ bool chunk_load(const KvRowsArgs& g, const int32_t* t
                     const unsigned char* from = live ? data + o + row_off : data;
 #pragma unroll
                     for (int k = 0; k < KP; ++k) {
-                        const bool there = live && (FULL || (lq + 4 * k) * 16 < c.D);
+                        const bool there = live && (FULL || (lq + 4 * k) * 16 < c.D) && kv_in(c, from + 64 * k - data, 16);
                         cp_async16_to(slot + (i * KP + k) * 2048, there ? from + 64 * k : data, there ? 16 : 0);
                     }
 #pragma unroll
                     for (int n = 0; n < SW; ++n) sc[SW * i + n] = 0;
-                    if (live) {
+                    if (live && kv_scale_in(c, so + row_soff, 1)) {
                         const unsigned char* sp = scale + so + row_soff;
                         if (FULL && D >= 128) {
 #pragma unroll
@@ -677,7 +677,7 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                     }
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = nothing ? 0.0f : o[k] * f;
-                    if (qr < nrows) {
+                    if (qr < nrows && kv_place_in(a.c, head, g.heads) && kv_place_in(a.c, at_p, g.s.splits * g.heads)) {
                         if (parts) {
                             float* to = g.po + at_p * width + i;
 #pragma unroll

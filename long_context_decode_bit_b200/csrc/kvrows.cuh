@@ -329,6 +329,7 @@ kv_rows_kernel(const KvRowsArgs g)
                 for (int j = 0; j < S::RPL; ++j)
 #pragma unroll
                     for (int i = 0; i < S::PP / S::LPR; ++i) {
+                        if (!kv_in(a.c, kp[j] - a.c.k + 16 * S::LPR * i, 16) || !kv_in(a.c, vp[j] - a.c.v + 16 * S::LPR * i, 16)) continue;
                         cp_async16_to(S::template step<S::LPR>(dst + k_to, i) + 8 * j * S::RB, kp[j] + 16 * S::LPR * i);
                         cp_async16_to(S::template step<S::LPR>(dst + v_to, i) + 8 * j * S::RB, vp[j] + 16 * S::LPR * i);
                     }
@@ -340,13 +341,14 @@ kv_rows_kernel(const KvRowsArgs g)
                     const unsigned char* vf = on ? vp[j] : a.c.v;
 #pragma unroll
                     for (int i = 0; i < S::PP / S::LPR; ++i) {
+                        if (on && (!kv_in(a.c, kf - a.c.k + 16 * S::LPR * i, 16) || !kv_in(a.c, vf - a.c.v + 16 * S::LPR * i, 16))) continue;
                         cp_async16_to(S::template step<S::LPR>(dst + k_to, i) + 8 * j * S::RB, kf + 16 * S::LPR * i, on ? 16 : 0);
                         cp_async16_to(S::template step<S::LPR>(dst + v_to, i) + 8 * j * S::RB, vf + 16 * S::LPR * i, on ? 16 : 0);
                     }
                 }
             }
             if (CODED) {
-                const bool on = (live >> (lane & 15)) & 1;
+                const bool on = ((live >> (lane & 15)) & 1) && kv_scale_in(a.c, sp_ - (lane < 16 ? a.c.ks : a.c.vs), S::NB);
                 sc[0] = sc[1] = 0;
                 if (on) {
                     if (S::NB == 4) {
@@ -621,6 +623,7 @@ kv_rows_kernel(const KvRowsArgs g)
         const float2 t = sm_t[row];   // maximum and weight sum
         const int tok = UNION ? 0 : qr / G;
         const int64_t head = ((sp.first + tok) * a.c.H + h) * G + (qr - tok * G), at_p = split * g.heads + head;
+        if (!kv_place_in(a.c, head, g.heads) || !kv_place_in(a.c, at_p, g.s.splits * g.heads)) continue;
         if (parts && lane == 0) {
             g.pm[at_p] = t.x;
             g.pl[at_p] = t.y;
