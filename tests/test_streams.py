@@ -119,3 +119,16 @@ def test_blocks_in_use_on_the_callers_stream_are_left_alone(fathom_gpu, name):
     got = tuple_of(call(stream=side))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_current_stream_by_torchs_public_api(monkeypatch):
+    """The current stream is found without the short way that torch offers itself, too."""
+    import importlib.util
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    spec = importlib.util.spec_from_file_location("fathom_again", fathom.__file__, submodule_search_locations=None)
+    again = importlib.util.module_from_spec(spec)
+    again.__package__ = fathom.__package__
+    spec.loader.exec_module(again)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: type("S", (), {"cuda_stream": 0x7000 + dev}))
+    assert again._stream(None) == 0x7003
