@@ -13,8 +13,9 @@
 // writes one token.  A row's place is three loads that wait for one another
 // (its sequence, its length, its page); many small threads hide the chain
 // better than several rows to a thread (a 128k int8 session of 8 groups read
-// back in bf16: 130 us, 6.3 TB/s, against 137 us with four; 32k tokens written and
-// read back 67 us against 80; a token 4.4 us against 6.6).
+// back in bf16: 131 us, 6.2 TB/s, against 137 us with four; 32k tokens written and
+// read back 70 us against 80, bf16 and e4m3 caches 90 and 70; a token 4.4 us
+// against 6.6).
 #include "kv.cuh"
 
 namespace fathom {
