@@ -136,6 +136,6 @@ constexpr int kScanTileTokens = kScanTileBlocks * kBlockTokens;
 
 CandLayout cand_layout(int64_t H, int G, int64_t n, int k);
 
-__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace fathom

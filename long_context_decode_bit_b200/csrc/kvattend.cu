@@ -112,7 +112,7 @@ kv_join_kernel(const KvRowsArgs g)
     if (head >= g.heads) {
         n = -1;
     } else if (a.uni) {
-        n = static_cast<int>(ceil_div(min(static_cast<int64_t>(max(a.count[head / a.G], 0)), a.M), g.s.chunk));
+        n = kv_stretches(min(static_cast<int64_t>(max(a.count[head / a.G], 0)), a.M), g.s.chunk);
     } else {
         const int row = static_cast<int>(head / heads_row), b = kv_sequence(a.w, row);
         const KvSpan sp = kv_span(a, max(b, 0));
@@ -120,7 +120,7 @@ kv_join_kernel(const KvRowsArgs g)
             n = -1;
         } else {
             const int qr = static_cast<int>(row - sp.first) * a.G + static_cast<int>(head % heads_row) % a.G;
-            n = static_cast<int>(ceil_div(kv_tile_keys(a, sp, qr / g.s.tile_rows * g.s.tile_rows, g.s.tile_rows), g.s.chunk));
+            n = kv_stretches(kv_tile_keys(a, sp, qr / g.s.tile_rows * g.s.tile_rows, g.s.tile_rows), g.s.chunk);
         }
     }
     // The lengths are the caller's; the parts are written by the kernel before.  Every CTA waits: the stream's next

@@ -136,6 +136,9 @@ __device__ __forceinline__ int kv_tile_keys(const KvAttend& a, const KvSpan& s, 
     return max(0, min(s.keys, s.pos0 + last / a.G + 1));
 }
 
+// Stretches of `chunk` that `keys` tokens take.
+__device__ __forceinline__ int kv_stretches(int64_t keys, int chunk) { return static_cast<int>((keys + chunk - 1) / chunk); }
+
 // NW words from shared memory.
 template <int NW>
 __device__ __forceinline__ void lds_words(uint32_t at, uint32_t* w)

@@ -38,3 +38,14 @@ def test_argument_surface():
     for case in bench.CASES:
         assert bench.parse_args(["--case", case]).case == case
     assert bench.parse_args(["--impl", "reference"]).impl == "reference"
+
+
+def test_committed_traffic_is_of_the_current_kernel():
+    """The scan's measured DRAM bytes are reported only while the sources they were taken on are the tree's."""
+    import json
+    import os
+    with open(os.path.join(bench.ROOT, "profiles", "scan_filter_traffic.json")) as f:
+        entries = json.load(f)
+    for name, entry in entries.items():
+        workload, budget = name.split("@")
+        assert bench.profiled_traffic(workload, int(budget)) == entry["dram_bytes_per_launch"]
