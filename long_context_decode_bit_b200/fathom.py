@@ -5,6 +5,10 @@ CUDA kernels.  torch tensors supply device memory and the current stream;
 outputs are allocated here with torch when the caller does not pass them.
 If the library is missing or cannot be loaded, every call raises -- there
 is no fallback.
+
+A function runs on the current stream or on the one it is given.  On a given
+stream its inputs have to be ready in that stream's order, and the caller's
+stream waits for it before it uses the outputs, as with torch's own calls.
 """
 from __future__ import annotations
 
