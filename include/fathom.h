@@ -608,6 +608,8 @@ int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, voi
  * are the weights exp(s - max) that enter the value product; with bf16 queries
  * they enter it in bf16 (half a step, up to 2^-8 of a weight) and their sum is
  * of the unrounded ones.  The result does not depend on timing.
+ * Scores are held in powers of two: a row with one above 2.3e38 (the largest
+ * fp32 over log2 e) is NaN.
  * Cached values of tokens below length should be finite where rows that do not
  * see them are to stay finite; what lies beyond length in a page is never
  * used.  A row that sees a NaN is NaN; a value that is infinite makes its

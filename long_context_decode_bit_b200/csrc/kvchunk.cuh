@@ -32,6 +32,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "kvrows.cuh"
 #include "ring.cuh"
@@ -42,6 +43,9 @@ constexpr int kChunkThreads = 512;
 // Query rows of a CTA and tokens of a tile, by the width of a row.
 constexpr int chunk_rows(int D) { return D <= 128 ? 256 : 128; }
 constexpr int chunk_keys(int D) { return D <= 128 ? 128 : 64; }
+// S scale log2 e - m is one fused operation, and m a rounded product: they differ by half a step of m, which is part of the
+// weight's exponent.  From here on (where a step is 2) the product is rounded too.
+constexpr float kFarScore = 16777216.0f;
 // Registers a thread of each role keeps; their sum is the launch's 4 x 128.
 constexpr int kRegsSoftmax = 192, kRegsLoad = 80, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 512, "more registers than the block has");
@@ -574,7 +578,7 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
         const float log2s = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
         const uint64_t log2s2 = pack2(log2s, log2s);
         float m = -INFINITY, l = 0.0f;
-        bool ok = true;
+        bool ok = true, far = false;   // far: a row of the warp has a maximum that fp32 holds to no better than 1
         if (t == 0 || two) {
             int page = chunk_page(a.c, table, a.w.table_pages, begin, end, lane);
             for (int j = 0; j < tiles; ++j) {
@@ -610,6 +614,7 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                     const float f = exp2_fast(m - (peak == -INFINITY ? 0.0f : peak));
                     l *= f;
                     m = peak;
+                    far = __any_sync(0xffffffffu, fabsf(m) >= kFarScore && m > -INFINITY);
                     if (j > 0) {
                         if (!S::PAIR) {   // of a pair, the product before is done: this tile's scores came after it
                             ok = __all_sync(0xffffffffu, mbar_wait(o_full + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1));
@@ -630,25 +635,34 @@ kv_chunk_kernel(const KvRowsArgs g, int32_t* __restrict__ fault)
                 const float low = m == -INFINITY ? 0.0f : -m;
                 const uint64_t low2 = pack2(low, low);
                 uint64_t sum[2] = {pack2(l, 0.0f), pack2(0.0f, 0.0f)};
+                auto weights = [&](auto rounded) {
 #pragma unroll
-                for (int part = 0; part < KEYS / 32; ++part) {
-                    uint32_t p[16];
+                    for (int part = 0; part < KEYS / 32; ++part) {
+                        uint32_t p[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float x, y;
-                        unpack2(fma2(pack2(s[32 * part + 2 * i], s[32 * part + 2 * i + 1]), log2s2, low2), x, y);
-                        x = exp2_fast(x);
-                        y = exp2_fast(y);
-                        sum[i & 1] = add2(sum[i & 1], pack2(x, y));
-                        p[i] = bf16x2(x, y);
+                        for (int i = 0; i < 16; ++i) {
+                            float x = s[32 * part + 2 * i], y = s[32 * part + 2 * i + 1];
+                            if constexpr (decltype(rounded)::value) {   // as the maximum was, so that no weight is above 2^8
+                                x = __fadd_rn(__fmul_rn(x, log2s), low);
+                                y = __fadd_rn(__fmul_rn(y, log2s), low);
+                            } else {
+                                unpack2(fma2(pack2(x, y), log2s2, low2), x, y);
+                            }
+                            x = exp2_fast(x);
+                            y = exp2_fast(y);
+                            sum[i & 1] = add2(sum[i & 1], pack2(x, y));
+                            p[i] = bf16x2(x, y);
+                        }
+                        tmem_st16(s_at + 16 * part, p);
+                        if (KEYS == 64 || (part & 1)) {   // half of the tile
+                            tmem_st_wait();
+                            tc_before();
+                            mbar_arrive(p_full + 16 * (KEYS == 64 ? part : part >> 1) + 8 * buf);
+                        }
                     }
-                    tmem_st16(s_at + 16 * part, p);
-                    if (KEYS == 64 || (part & 1)) {   // half of the tile
-                        tmem_st_wait();
-                        tc_before();
-                        mbar_arrive(p_full + 16 * (KEYS == 64 ? part : part >> 1) + 8 * buf);
-                    }
-                }
+                };
+                if (far) weights(std::true_type{});
+                else weights(std::false_type{});
                 float l0, l1;
                 unpack2(add2(sum[0], sum[1]), l0, l1);
                 l = l0 + l1;

@@ -99,3 +99,58 @@ def test_infinities_in_bf16_pages(fathom_gpu, new):
         rest[5:7] = False
         assert first[..., rest].isfinite().all()
         assert out[new:2 * new].isnan().all() and out[2 * new:].isfinite().all()
+
+
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_scores_up_to_where_they_overflow(fathom_gpu, dtype, new):
+    """The largest scale: the one key with a score of 2.2e38 is the row's answer, one of 2.4e38 makes it NaN, one of -2.4e38
+    takes no part."""
+    D, n = 64, 80
+    lens = [(new, n)]
+    pages, table, cu, length = make_batch(lens, 16)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    everything = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    q = torch.zeros((new, 2, D), device=DEV, dtype=dtype)
+    q[..., 0] = 1.0
+    for top in (2.203125, 2.40625, -2.40625):      # bf16 values
+        k, v = torch.zeros((n, 1, D), device=DEV), torch.randn((n, 1, D), generator=g, device=DEV).bfloat16().float()
+        k[7, 0, 0] = top
+        cache = make_cache(fathom_gpu, "bf16", pages, 1, D, 16)
+        fathom_gpu.kv_write(cache, k, v, table, everything, length)
+        out = fathom_gpu.paged_attention(cache, q, table, cu, length, new, n, causal=False, scale=1e38).double()
+        if top > 2.3:
+            assert out.isnan().all()
+        elif top > 0:
+            assert torch.equal(out, v[7].double().expand_as(out))
+        else:
+            rest = torch.cat([v[:7], v[8:]]).double().mean(0)
+            assert ((out - rest).abs() <= rest.abs() * 2.0 ** -8 + 2.0 ** -8).all()   # weights of 1, 79 of them; output in bf16
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("new", [1, 10, 100])
+@pytest.mark.parametrize("fmt,D", [("bf16", 64), ("int8", 128), ("e4m3", 96), ("bf16", 256), ("int8", 160)])
+def test_scores_whose_steps_are_large(fathom_gpu, fmt, D, new, dtype):
+    """Scores so large that fp32 holds them in steps of 2 and more: the largest one's value is the answer, two that are equal
+    share it, and causal rows over scores that grow from token to token have their own token's value."""
+    n = 400
+    lens = [(new, n)]
+    pages, table, cu, length = make_batch(lens, 64)
+    g = torch.Generator(device=DEV).manual_seed(D)
+    everything = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    base = torch.where(torch.rand(D, generator=g, device=DEV) < 0.5, -1.0, 1.0)      # q . k = D times the keys' factor
+    v = torch.randint(-7, 8, (n, 1, D), generator=g, device=DEV).float()             # values that every format holds
+    q = (base * torch.tensor([1.0, 0.5, 2.0], device=DEV)[:, None]).expand(new, 3, D).contiguous().to(dtype)
+    two = torch.full((n,), 0.5, device=DEV)
+    two[7] = two[251] = 1.75
+    at = torch.arange(n, device=DEV)
+    grow = 2.0 ** (at // 8 - 35).float() * (1 + at % 8 / 8)   # 4 bits each, up to 30720 (E4M3 ends at 57344)
+    scales = (2.0 ** 20, 2.0 ** 23, 2.0 ** 26, 1.37e9, 2.0 ** 40, -2.0 ** 30)
+    for factor, causal, want, more in ((two, False, (v[7] + v[251]) / 2, (1.37e20, 2.0 ** 100, -2.0 ** 110)),
+                                       (grow, True, v[n - new:], ())):
+        cache = make_cache(fathom_gpu, fmt, pages, 1, D, 64)
+        fathom_gpu.kv_write(cache, (factor[:, None, None] * base).contiguous(), v, table, everything, length)
+        for scale in scales + more:
+            out = fathom_gpu.paged_attention(cache, q if scale > 0 else -q, table, cu, length, new, n, causal=causal, scale=scale)
+            assert torch.equal(out.float(), want.expand(new, 3, D)), (scale, causal)
