@@ -610,6 +610,8 @@ int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, voi
  * of the unrounded ones.  The result does not depend on timing.
  * Scores are held in powers of two: a row with one above 2.3e38 (the largest
  * fp32 over log2 e) is NaN.
+ * Sums of weights times values are fp32 too, of weights up to 2^8: values
+ * above 1e36 over the number of tokens may overflow before they are divided.
  * Cached values of tokens below length should be finite where rows that do not
  * see them are to stay finite; what lies beyond length in a page is never
  * used.  A row that sees a NaN is NaN; a value that is infinite makes its

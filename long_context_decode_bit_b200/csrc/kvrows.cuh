@@ -489,7 +489,7 @@ kv_rows_kernel(const KvRowsArgs g)
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[nt][i] *= log2s;
+                s[nt][i] = __fmul_rn(s[nt][i], log2s);   // never fused with what follows: a step of the maximum may be large
                 if (!whole) {
                     const int key = r + 8 * (i >> 1);
                     if (!((live >> key) & 1) || at + key > seen[nt][i & 1]) s[nt][i] = -INFINITY;
