@@ -608,6 +608,9 @@ int fathom_kv_read(const fathom_kv_cache* cache, const fathom_kv_rows* rows, voi
  * are the weights exp(s - max) that enter the value product; with bf16 queries
  * they enter it in bf16 (half a step, up to 2^-8 of a weight) and their sum is
  * of the unrounded ones.  The result does not depend on timing.
+ * The value sums of fp32 queries are rounded to nearest every 16 tokens; those
+ * of bf16 queries are the matrix units', which cut off: up to 2^-24 of the sum
+ * for every 16 tokens of a stretch, 1e-3 over 2^18.
  * Scores are held in powers of two: a row with one above 2.3e38 (the largest
  * fp32 over log2 e) is NaN.
  * Sums of weights times values are fp32 too, of weights up to 2^8: values

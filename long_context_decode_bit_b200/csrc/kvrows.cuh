@@ -23,7 +23,10 @@
 // weights below 2^-40 are lost; both took the same time.)  A dot product may
 // run over the channels in any order, so a lane takes consecutive bytes of a
 // row, and Q is laid out to match.  fp32 queries and their weights are three
-// bf16 parts each (24 bits); the weights of bf16 queries are rounded to bf16,
+// bf16 parts each (24 bits), and a tile's three products are summed apart from
+// the tiles before, to which they are added with a rounding: the matrix units
+// cut sums off, which over a session of a million tokens came to 1e-4 (now
+// 7e-7, for 1 to 2% of the time).  The weights of bf16 queries are rounded to bf16,
 // up to 2^-8 of each, like the output they go into.  (Two parts of a weight
 // would leave the output's own rounding, 1.65e-3 of its size instead of 1.85e-3
 // over an int8 session, and take the 128k int8 token from 69.4 to 72.1 us.)
@@ -532,9 +535,15 @@ kv_rows_kernel(const KvRowsArgs g)
         }
         auto values = [&](int t, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-            for (int p = 0; p < S::NP; ++p)
+            for (int nt = 0; nt < NT; ++nt) {
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma16816(o[t][nt], a0, a1, a2, a3, pb[nt][p][0], pb[nt][p][1]);
+                for (int p = 0; p < S::NP; ++p) mma16816(S::WIDEQ ? sum : o[t][nt], a0, a1, a2, a3, pb[nt][p][0], pb[nt][p][1]);
+                if (S::WIDEQ) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[t][nt][i] += sum[i];
+                }
+            }
         };
         if constexpr (CODED) {
 #pragma unroll

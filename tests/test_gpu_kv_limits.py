@@ -154,3 +154,25 @@ def test_scores_whose_steps_are_large(fathom_gpu, fmt, D, new, dtype):
         for scale in scales + more:
             out = fathom_gpu.paged_attention(cache, q if scale > 0 else -q, table, cu, length, new, n, causal=causal, scale=scale)
             assert torch.equal(out.float(), want.expand(new, 3, D)), (scale, causal)
+
+
+@pytest.mark.parametrize("new", [1, 64])
+def test_long_sums_of_fp32_queries(fathom_gpu, new):
+    """A million tokens whose values are all the same: that value, within the roundings to nearest of a stretch's sums.  The
+    weights and the values go into sums of their own, each with a rounding of at most 2^-24 for every 16-token tile of a
+    warp (a quarter of a stretch), then for every stretch and warp that is joined; 64 for a tile's own sum, the weights'
+    exponentials and the division."""
+    H, G, D, page, n = 8, 4, 128, 256, 1 << 20
+    g = torch.Generator(device=DEV).manual_seed(1)
+    k = torch.randint(-60, 61, (n // page, H, page, D), generator=g, dtype=torch.int8, device=DEV)
+    exps = [torch.full((n // page, H, page, D // 32), 127 - e, dtype=torch.uint8, device=DEV) for e in (5, 6)]
+    cache = fathom_gpu.KVCache(k, torch.full_like(k, 93), *exps)
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV)[None]
+    q = torch.randn((new, H * G, D), generator=g, device=DEV)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    out = fathom_gpu.paged_attention(cache, q, table, i32(0, new), i32(n), new, n, causal=False)
+    scratch = fathom_gpu.paged_attention_workspace_bytes(H, G, D, new, 1, new, n, torch.float32)
+    stretches = scratch // (new * H * G * (4 * D + 8))
+    tiles = -(-n // stretches // 64)
+    bound = (2 * tiles + 2 * (-(-stretches // 16) + 16) + 64) * 2.0 ** -24
+    assert ((out.double() / (93 / 64) - 1).abs() <= bound).all()
