@@ -72,7 +72,7 @@ KvSplit rows_split(int H, int G, int D, int64_t rows, int B, int64_t max_new, in
 
 // A union has between 1/G of M rows and all of them, only the device knows:
 // 5/8 is taken (the mean at G = 4; 288 groups of 25%, 62% and 99% of 2048 rows
-// take 33, 47 and 72 us), and one wave of CTAs, four to an SM, for that (a group's last
+// take 33, 48 and 73 us), and one wave of CTAs, four to an SM, for that (a group's last
 // stretch is half one on average).
 KvSplit union_split(int64_t H, int64_t M)
 {
